@@ -84,11 +84,17 @@ __device__ __forceinline__ float i4_round_bf16(float x) {
   return __bfloat162float(__float2bfloat16_rn(x));
 }
 
-// Code + 8 of x (+ l), x = h (+ l), for a group of scale s > 0 (inv near 1/s):
-// the half-way point below or above the approximate quotient decides by the
-// sign of an exactly rounded difference, ties to the even code.
-__device__ __forceinline__ uint32_t i4_code_of(float h, float l, float s, float inv) {
-  const float k = fminf(fmaxf(floorf(h * inv), -7.f), 6.f);
+// Groups of scales below kI4Tiny are worked on times kI4Up, a power of two, so
+// that no reciprocal overflows and no product or rounding error underflows
+// (scales go down to bf16's smallest value, 2^-133).
+constexpr float kI4Tiny = 0x1p-100f, kI4Up = 0x1p100f;
+constexpr uint32_t kI4TinyBits = (127 - 97) << 23;   // of 8 kI4Tiny: no larger group has such a scale
+
+// Code + 8 of x (+ l), x = h (+ l), for a group of scale s > 0: the half-way
+// point below or above the approximate quotient decides by the sign of an
+// exactly rounded difference, ties to the even code.
+__device__ __forceinline__ uint32_t i4_code_of(float h, float l, float s) {
+  const float k = fminf(fmaxf(floorf(h * (1.0f / s)), -7.f), 6.f);
   const float d = fmaf(-(k + 0.5f), s, h) + l;
   const int ki = static_cast<int>(k);
   const int up = d > 0.f || (d == 0.f && (ki & 1)) ? 1 : 0;
@@ -223,12 +229,12 @@ __device__ __forceinline__ void prologue_i4(
     // V: a seventh of an 8-bit value is never this near to a tie
     near = near || (row == 0 && am < 0x7f800000u &&
                     i4_round_bf16(a7 * (1.f + 1.25f * kI4RelErr)) != i4_round_bf16(a7 * (1.f - 1.25f * kI4RelErr)));
+    near = near || am - 1u < kI4TinyBits;   // (tiny groups, K's and V's)
     if (s[h] > 0.f) {
       // the code nearest to x / s, and how far x is from it: near a tie (for K
-      // within 7 s of the error of a value) it is looked at again below; so are
-      // the groups of scales that bf16 rounds coarsely.  Elsewhere |x / s| < 7.1.
+      // within 7 s of the error of a value) it is looked at again below.
+      // Elsewhere |x / s| < 7.1.
       const float si = rcp_approx(s[h]), lim = s[h] * (0.5f - 8.f * 1.25f * kI4RelErr);
-      near = near || s[h] < 0x1p-100f;
       u[h] = 0;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -244,63 +250,80 @@ __device__ __forceinline__ void prologue_i4(
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if (!(s[h] > 0.f)) continue;
-      const float si = 1.0f / s[h];
+      const float t = s[h] < kI4Tiny ? kI4Up : 1.f;
       u[h] = 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) u[h] |= i4_code_of(y[4 * h + e], 0.f, s[h], si) << (4 * e);
+      for (int e = 0; e < 4; ++e) u[h] |= i4_code_of(y[4 * h + e] * t, 0.f, s[h] * t) << (4 * e);
     }
   }
   if ((again & 0xffffu) != 0u) {
     // K again in pairs of floats (both halves of the warp go along; V's keeps
-    // what it has)
+    // what it has), pairs of tiny elements rotated times kI4Up
     F2 z[8];
+    unsigned raised = 0;   // bit e: elements e and 4 + e
     F2 sum = {0.f, 0.f};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const F2 c = {cs[e], 0.f}, t = {sn[e], 0.f}, a = {x[e], 0.f}, bb = {x[4 + e], 0.f};
+      const bool tiny = fmaxf(fabsf(x[e]), fabsf(x[4 + e])) < 0x1p-60f;
+      raised |= tiny ? 1u << e : 0u;
+      const float f = tiny ? kI4Up : 1.f;
+      const F2 c = {cs[e], 0.f}, t = {sn[e], 0.f}, a = {x[e] * f, 0.f}, bb = {x[4 + e] * f, 0.f};
       const F2 at = f2_mul(a, t), bt = f2_mul(bb, t);
       z[e] = f2_add(f2_mul(a, c), F2{-bt.h, -bt.l});
       z[4 + e] = f2_add(f2_mul(bb, c), at);
-      sum = f2_add(sum, f2_add(f2_mul(z[e], z[e]), f2_mul(z[4 + e], z[4 + e])));
+      F2 sq = f2_add(f2_mul(z[e], z[e]), f2_mul(z[4 + e], z[4 + e]));
+      if (tiny) sq = {sq.h / kI4Up / kI4Up, sq.l / kI4Up / kI4Up};
+      sum = f2_add(sum, sq);
     }
 #pragma unroll
     for (int off = 8; off > 0; off >>= 1)
       sum = f2_add(sum, F2{__shfl_xor_sync(0xffffffffu, sum.h, off), __shfl_xor_sync(0xffffffffu, sum.l, off)});
     const F2 r = f2_rsqrt(f2_add(F2{sum.h * (1.0f / kD), sum.l * (1.0f / kD)}, F2{eps, 0.f}));
 #pragma unroll
-    for (int e = 0; e < 8; ++e) z[e] = f2_mul(z[e], f2_mul(r, F2{w[e], 0.f}));
-#pragma unroll
     for (int h = 0; h < 2; ++h) {
+      // k', of a tiny group times kI4Up, half of it in each factor (so neither
+      // overflows), less what its rotation was raised by
+      const bool lift = s[h] < kI4Tiny;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const bool was = raised >> e & 1u;
+        const float f = lift == was ? 1.f : lift ? 0x1p50f : 0x1p-50f;
+        const F2 zr = f2_mul(z[4 * h + e], r);
+        z[4 * h + e] = f2_mul(F2{zr.h * f, zr.l * f}, F2{w[4 * h + e] * f, 0.f});
+      }
       // the largest magnitude of the group as a pair: sign of h on both parts
       F2 m = {0.f, 0.f};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        F2 t = z[4 * h + e];
-        if (t.h < 0.f) t = {-t.h, -t.l};
-        if (t.h > m.h || (t.h == m.h && t.l > m.l)) m = t;
+        F2 v = z[4 * h + e];
+        if (v.h < 0.f) v = {-v.h, -v.l};
+        if (v.h > m.h || (v.h == m.h && v.l > m.l)) m = v;
       }
 #pragma unroll
       for (int off = 1; off < 8; off <<= 1) {
-        const F2 t = {__shfl_xor_sync(0xffffffffu, m.h, off), __shfl_xor_sync(0xffffffffu, m.l, off)};
-        if (t.h > m.h || (t.h == m.h && t.l > m.l)) m = t;
+        const F2 v = {__shfl_xor_sync(0xffffffffu, m.h, off), __shfl_xor_sync(0xffffffffu, m.l, off)};
+        if (v.h > m.h || (v.h == m.h && v.l > m.l)) m = v;
       }
       // (a row with infinities or NaN never gets here for its own sake: its
       // half of the group keeps the NaN scale)
       if (row != 0 || !(s[h] >= 0.f)) continue;
       // a seventh rounded to bf16: the candidate below, and the half-way point
-      // above it against the pair (7 times it is exact in fp32)
-      const float c0 = __uint_as_float(__float_as_uint(m.h * (1.0f / kI4Levels) * (1.f - 0x1p-20f)) & 0xffff0000u);
-      const float step = __uint_as_float((__float_as_uint(c0) & 0x7f800000u)) * 0x1p-7f;
-      const float mid = c0 + 0.5f * step, next = c0 + step;
-      const float up = __fadd_rn(__fsub_rn(m.h, 7.f * mid), m.l);
-      float sc = up > 0.f || (up == 0.f && (__float_as_uint(c0) & 0x10000u)) ? next : c0;
-      if (!(c0 > 0x1p-120f)) sc = s[h];   // tiny groups: fp32's answer
-      s[h] = sc;
+      // above it against the pair (7 times it is exact in fp32).  Steps below
+      // 2^-126 are 2^-133.
+      const float m7 = m.h * (1.0f / kI4Levels) * (1.f - 0x1p-20f);
+      const bool coarse = lift && m7 < 0x1p-126f * kI4Up;
+      const float unit = 0x1p-133f * kI4Up;
+      const float c0 = coarse ? floorf(m7 * (1.f / unit)) * unit : __uint_as_float(__float_as_uint(m7) & 0xffff0000u);
+      const float step = coarse ? unit : __uint_as_float(__float_as_uint(c0) & 0x7f800000u) * 0x1p-7f;
+      const bool odd = coarse ? static_cast<int>(c0 * (1.f / unit)) & 1 : __float_as_uint(c0) >> 16 & 1u;
+      const float d = __fadd_rn(__fsub_rn(m.h, 7.f * (c0 + 0.5f * step)), m.l);
+      const float sc = d > 0.f || (d == 0.f && odd) ? c0 + step : c0;
+      s[h] = lift ? sc * (1.f / kI4Up) : sc;
+      u[h] = 0x8888u;
       if (sc > 0.f) {
-        const float si = 1.0f / sc;
         u[h] = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) u[h] |= i4_code_of(z[4 * h + e].h, z[4 * h + e].l, sc, si) << (4 * e);
+        for (int e = 0; e < 4; ++e) u[h] |= i4_code_of(z[4 * h + e].h, z[4 * h + e].l, sc) << (4 * e);
       }
     }
   }
