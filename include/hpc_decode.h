@@ -315,7 +315,9 @@ int hpc_decode_plan_static(const int32_t* seq_lens, int32_t batch, int32_t max_b
  *                overlap on the GPU (they share its pool counters).
  *   partial_o    (device) float32 [plan->capacity, 8, 128], written per item,
  *                16-byte aligned
- *   partial_lse  (device) float32 [plan->capacity, 8], written per item,
+ *   partial_lse  (device) float32 [plan->capacity, 8], written per item: -inf for
+ *                an item without keys; over 4-bit pages NaN for a row with a NaN
+ *                among its scores (a NaN or an infinity in q, a NaN in K),
  *                16-byte aligned (both alignments hold for every call that
  *                takes partial buffers: the attention writes and reads them,
  *                and the merges read them, 16 bytes at a time)
@@ -368,7 +370,8 @@ int hpc_decode_attn_profiled(const void* q, const void* kv_cache, int32_t kv_dty
  * seg_ptr[s] .. seg_ptr[s+1]-1, in item order,
  *   M = max_k lse_k,  w_k = exp(lse_k - M),
  *   out[b][8h + r] = bf16( sum_k w_k partial_o[k][r] / sum_k w_k )
- * A segment with no items (an empty sequence) gets zeros.
+ * A segment with no items (an empty sequence), or with empty ones only, gets
+ * zeros; a NaN among the lse_k makes the row NaN.
  *   out  (device) bf16 [batch, 64, 128], written.
  * Errors: HPC_ERR_INVALID_ARG for null pointers or batch < 0. */
 int hpc_merge(const float* partial_o, const float* partial_lse, const hpc_plan* plan,

@@ -663,13 +663,16 @@ struct I4Warp<2> : I4Rows<1> {};
 template <>
 struct I4Warp<4> : I4Rows<2> {};
 
-// Log-sum-exp (natural) of a state kept in log2 units; -inf for an empty one.
+// Log-sum-exp (natural) of a state kept in log2 units; -inf for an empty one,
+// NaN where the sum is (a NaN in q or in a K that it sees): the merges must not
+// take such a state for an empty one.
 __device__ __forceinline__ float i4_lse(float m, float l) {
-  return l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+  return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
 // One row of a segment of several items, by one warp: the items' partials in
-// item order (row p0, then per_seg rows on), with four elements a lane.
+// item order (row p0, then per_seg rows on), with four elements a lane.  A NaN
+// among the log-sum-exps makes the row NaN.
 __device__ __forceinline__ void i4_merge_row(const float* partial_o, const float* partial_lse, int64_t p0, int cnt,
                                           int per_seg, void* out, int64_t orow, int out_dtype) {
   const int lane = threadIdx.x & 31;
@@ -685,9 +688,9 @@ __device__ __forceinline__ void i4_merge_row(const float* partial_o, const float
   for (int k = 0; k < 2; ++k)
     if (k < cnt) pre[k] = o_of(k);
   float M = lse;
-  for (int k = lane + 32; k < cnt; k += 32) M = fmaxf(M, lse_of(k));
+  for (int k = lane + 32; k < cnt; k += 32) M = max_nan(M, lse_of(k));
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  for (int off = 16; off > 0; off >>= 1) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, off));
   float wsum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   auto add = [&](float w, float4 v) {

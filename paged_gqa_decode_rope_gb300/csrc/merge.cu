@@ -11,7 +11,8 @@
 // handles query head 8h + r and each lane 4 consecutive elements, so every
 // partial row is one coalesced 512-byte read.  Items are combined in item
 // order (that is, tile order), which makes the output bit-reproducible.  A
-// segment whose every partial is empty (lse = -inf) merges to zeros.  With
+// segment whose every partial is empty (lse = -inf) merges to zeros, one with a
+// NaN among its log-sum-exps to NaN.  With
 // q_len new tokens per sequence the partial of item i for token j is row
 // (i*q_len + j)*8 + r, and the output row is (b*q_len + j)*64 + 8h + r.
 #include "common.cuh"
@@ -56,8 +57,8 @@ __global__ void __launch_bounds__(256, 4) merge_kernel(const float* __restrict__
       for (int k = lane; k < cn; k += 32) lse_s[r][k] = partial_lse[prow(c0 + k)];
       __syncwarp();
       float Mc = -INFINITY;
-      for (int k = 0; k < cn; ++k) Mc = fmaxf(Mc, lse_s[r][k]);
-      const float Mn = fmaxf(M, Mc);
+      for (int k = 0; k < cn; ++k) Mc = max_nan(Mc, lse_s[r][k]);
+      const float Mn = max_nan(M, Mc);
       if (Mn == -INFINITY) continue;   // nothing but empty partials so far
       const float sc = M == -INFINITY ? 0.f : expf(M - Mn);
       acc.x *= sc;

@@ -1,0 +1,81 @@
+"""A NaN or an infinity in a query, or a NaN in a cached K, makes that row NaN,
+however the plan cuts its sequence, and leaves every other row as it is."""
+
+import pytest
+import torch
+
+import gpu_util as gu
+import int4_util as iu
+from oracle import int4 as oi
+
+pytestmark = pytest.mark.gpu
+LENS = [9000, 130, 64, 1, 0, 700]
+INT4 = 2
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    gu.require_gpu()
+
+
+def _run(step, q, cache, scale, table, lens):
+    step.out.fill_(7.0)
+    step.partial_o.fill_(7.0)
+    step.partial_lse.fill_(7.0)
+    step.plan_step(lens)
+    out = step.attend(q, cache, scale, table, lens).clone()
+    assert int(step.status.item()) == 0
+    return out
+
+
+def _several(step, b):
+    """Items that KV head 0 of sequence b is cut into."""
+    return int(step.plan.seg_ptr[8 * b + 1]) - int(step.plan.seg_ptr[8 * b])
+
+
+@pytest.mark.parametrize("n_ctas", [None, 3])
+@pytest.mark.parametrize("fused", [True, False])
+@pytest.mark.parametrize("q_len", [1, 2, 3, 4])
+def test_int4_query_that_is_not_finite(q_len, fused, n_ctas):
+    from paged_gqa_decode_rope_gb300 import ops
+    b = iu.Int4Batch(LENS, 81)
+    q = iu.queries((len(LENS), q_len, 64, 128), 82)
+    step = ops.DecodeStepEx(len(LENS), INT4, b.max_blocks, q_len=q_len, out_dtype=ops.OUT_FP32, fused=fused,
+                            n_ctas=n_ctas)
+    args = (b.cache, None, b.block_table, b.seq_lens)
+    want = _run(step, q, *args)
+    assert _several(step, 0) > 1 or n_ctas
+    bad = torch.zeros(want.shape[:3], dtype=torch.bool, device="cuda")
+    for s in (0, 1, 2, 5):
+        q[s, q_len - 1, 5, 77] = float("nan")
+        q[s, q_len - 1, 62, 0] = float("-inf" if s else "inf")
+        bad[s, q_len - 1, 5] = bad[s, q_len - 1, 62] = True
+    got = _run(step, q, *args)
+    assert bool(torch.isnan(got[bad]).all()), "a row that is not finite reads as %s" % got[bad][:, 0].tolist()
+    assert torch.equal(got[~bad], want[~bad])
+
+
+@pytest.mark.parametrize("fused", [True, False])
+@pytest.mark.parametrize("q_len", [1, 2, 4])
+def test_int4_key_that_is_nan(q_len, fused):
+    """In every token of one head of a sequence of many items, in the first token
+    only of another."""
+    from paged_gqa_decode_rope_gb300 import ops
+    b = iu.Int4Batch(LENS, 83)
+    q = iu.queries((len(LENS), q_len, 64, 128), 84)
+    step = ops.DecodeStepEx(len(LENS), INT4, b.max_blocks, q_len=q_len, fused=fused)
+    args = (None, b.block_table, b.seq_lens)
+    want = _run(step, q, b.cache, *args)
+    assert _several(step, 0) > 1
+    cache = b.cache.clone()
+    nan = torch.tensor([0xC0, 0x7F], dtype=torch.uint8, device="cuda")
+    for t in range(LENS[0]):
+        blk = int(b.table[0, t // 64])
+        for h in (2, 6) if t == 0 else (2,):
+            at = oi.scale_byte(0, t % 64, 1)
+            cache[blk, h, at:at + 2] = nan
+    got = _run(step, q, cache, *args)
+    bad = torch.zeros(want.shape[:3], dtype=torch.bool, device="cuda")
+    bad[0, :, 16:24] = bad[0, :, 48:56] = True
+    assert bool(torch.isnan(got[bad]).all())
+    assert torch.equal(got[~bad], want[~bad])
