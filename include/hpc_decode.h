@@ -316,8 +316,8 @@ int hpc_decode_plan_static(const int32_t* seq_lens, int32_t batch, int32_t max_b
  *   partial_o    (device) float32 [plan->capacity, 8, 128], written per item,
  *                16-byte aligned
  *   partial_lse  (device) float32 [plan->capacity, 8], written per item: -inf for
- *                an item without keys; over 4-bit pages NaN for a row with a NaN
- *                among its scores (a NaN or an infinity in q, a NaN in K),
+ *                an item without keys, NaN for a row with a NaN among its scores
+ *                (a NaN or an infinity in q, a NaN in K),
  *                16-byte aligned (both alignments hold for every call that
  *                takes partial buffers: the attention writes and reads them,
  *                and the merges read them, 16 bytes at a time)

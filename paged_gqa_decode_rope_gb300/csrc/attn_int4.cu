@@ -663,32 +663,25 @@ struct I4Warp<2> : I4Rows<1> {};
 template <>
 struct I4Warp<4> : I4Rows<2> {};
 
-// Log-sum-exp (natural) of a state kept in log2 units; -inf for an empty one,
-// NaN where the sum is (a NaN in q or in a K that it sees): the merges must not
-// take such a state for an empty one.
-__device__ __forceinline__ float i4_lse(float m, float l) {
-  return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-}
-
 // One row of a segment of several items, by one warp: the items' partials in
 // item order (row p0, then per_seg rows on), with four elements a lane.  A NaN
 // among the log-sum-exps makes the row NaN.
 __device__ __forceinline__ void i4_merge_row(const float* partial_o, const float* partial_lse, int64_t p0, int cnt,
                                           int per_seg, void* out, int64_t orow, int out_dtype) {
   const int lane = threadIdx.x & 31;
-  auto lse_of = [&](int k) { return __ldcg(partial_lse + p0 + static_cast<int64_t>(k) * per_seg); };
+  auto item_lse = [&](int k) { return __ldcg(partial_lse + p0 + static_cast<int64_t>(k) * per_seg); };
   auto o_of = [&](int k) {
     return __ldcg(reinterpret_cast<const float4*>(partial_o + (p0 + static_cast<int64_t>(k) * per_seg) * kD +
                                                   4 * lane));
   };
   // the first items' loads all go out at once (most segments have two)
-  const float lse = lane < cnt ? lse_of(lane) : -INFINITY;
+  const float lse = lane < cnt ? item_lse(lane) : -INFINITY;
   float4 pre[2];
 #pragma unroll
   for (int k = 0; k < 2; ++k)
     if (k < cnt) pre[k] = o_of(k);
   float M = lse;
-  for (int k = lane + 32; k < cnt; k += 32) M = max_nan(M, lse_of(k));
+  for (int k = lane + 32; k < cnt; k += 32) M = max_nan(M, item_lse(k));
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, off));
   float wsum = 0.f;
@@ -702,7 +695,7 @@ __device__ __forceinline__ void i4_merge_row(const float* partial_o, const float
   };
   for (int k0 = 0; k0 < cnt && M != -INFINITY; k0 += 32) {
     const int n = min(32, cnt - k0);
-    const float w = lane < n ? __expf((k0 == 0 ? lse : lse_of(k0 + lane)) - M) : 0.f;
+    const float w = lane < n ? __expf((k0 == 0 ? lse : item_lse(k0 + lane)) - M) : 0.f;
     if (k0 == 0) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
@@ -1175,7 +1168,7 @@ __global__ void __launch_bounds__(I4Cfg<kNq>::kThreads, 1) decode_attn_i4_kernel
           });
           if (!direct)
             st.stats(lane, [&](int j, int hh, float mx, float l) {
-              if (j < q_len) partial_lse[(static_cast<int64_t>(m.x) * q_len + j) * kGroup + hh] = i4_lse(mx, l);
+              if (j < q_len) partial_lse[(static_cast<int64_t>(m.x) * q_len + j) * kGroup + hh] = lse_of(mx, l);
             });
         } else {
           // Shared with other warps: a state to hand over when the range is
@@ -1267,7 +1260,7 @@ __global__ void __launch_bounds__(I4Cfg<kNq>::kThreads, 1) decode_attn_i4_kernel
             const int64_t prow = (static_cast<int64_t>(head.x) * q_len + j) * kGroup + hh;
             *reinterpret_cast<float4*>(partial_o + prow * kD + 4 * lane) =
                 make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-            if (lane == 0) partial_lse[prow] = i4_lse(Ms, L);
+            if (lane == 0) partial_lse[prow] = lse_of(Ms, L);
           }
         }
       }

@@ -952,6 +952,7 @@ __global__ void __launch_bounds__(AttnTraits<kFp8, kTC>::kThreads, 1) decode_att
             const int se = 7 - max(e2, -119);   // in [-120, 126]
             const float sc = __uint_as_float(static_cast<uint32_t>(127 + se) << 23);
             c_row = scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - se) << 23);
+            if (amax == INFINITY) c_row = __uint_as_float(0x7fc00000u);   // (E4M3 would take it for 448)
             // codes of 4 values (a 32-bit word), leading term and remainder
             auto split4 = [&](uint32_t u0, uint32_t u1, uint32_t& hi, uint32_t& lo) {
               const float a0 = bf16_lo(u0) * sc, a1 = bf16_hi(u0) * sc;
@@ -1089,7 +1090,7 @@ __global__ void __launch_bounds__(AttnTraits<kFp8, kTC>::kThreads, 1) decode_att
           }
         }
         if (valid && !direct)
-          partial_lse[prow] = lsum > 0.f ? (m_used + log2f(lsum)) * 0.6931471805599453f : -INFINITY;
+          partial_lse[prow] = lse_of(m_used, lsum);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(b_ofree);
@@ -1439,7 +1440,7 @@ __global__ void __launch_bounds__(AttnTraits<kFp8, kTC>::kThreads, 1) decode_att
               make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
           if ((e & 127) == 0)
             partial_lse[(static_cast<int64_t>(i) * q_len + j) * kGroup + hh] =
-                L > 0.f ? (Ms + log2f(L)) * 0.6931471805599453f : -INFINITY;
+                lse_of(Ms, L);
         }
       }
     }
@@ -1513,7 +1514,7 @@ __global__ void __launch_bounds__(AttnTraits<kFp8, kTC>::kThreads, 1) decode_att
             const int e = ej - j * kGroup * kD;
             const int row_l = j * kGroup + (e >> 7);   // lse row within an item
             float Mn = M[u];
-            for (int k = 0; k < m; ++k) Mn = fmaxf(Mn, lse_s[k * rows + row_l]);
+            for (int k = 0; k < m; ++k) Mn = max_nan(Mn, lse_s[k * rows + row_l]);
             if (Mn != -INFINITY) {
               const float sc = __expf(M[u] - Mn);   // 0 while M is still -inf
               acc[u].x *= sc; acc[u].y *= sc; acc[u].z *= sc; acc[u].w *= sc;

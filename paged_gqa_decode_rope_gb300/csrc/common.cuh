@@ -322,6 +322,12 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
   return d;
 }
+// Log-sum-exp (natural) of a softmax state kept in log2 units: -inf for an empty
+// one, NaN where the sum is (a NaN or an infinity in q, a NaN in a K that it
+// sees): the merges must not take such a state for an empty one.
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
 __device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
   uint64_t d;
   asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));

@@ -79,3 +79,30 @@ def test_int4_key_that_is_nan(q_len, fused):
     bad[0, :, 16:24] = bad[0, :, 48:56] = True
     assert bool(torch.isnan(got[bad]).all())
     assert torch.equal(got[~bad], want[~bad])
+
+
+@pytest.mark.parametrize("fused", [True, False])
+@pytest.mark.parametrize("kv,q_dtype,q_len", [(0, 0, 1), (0, 0, 2), (0, 0, 3), (0, 0, 4), (1, 0, 1), (1, 0, 2),
+                                              (1, 0, 3), (1, 0, 4), (1, 1, 1), (1, 1, 2), (1, 1, 4)])
+def test_query_that_is_not_finite(kv, q_dtype, q_len, fused):
+    """BF16 and E4M3 pages, an E4M3 query among them (which has no infinity)."""
+    from paged_gqa_decode_rope_gb300 import ops
+    from paged_gqa_decode_rope_gb300.workloads import Workload
+    wl = Workload("custom", seed=85, lengths=LENS, kv_dtype=kv, include_new_token=True)
+    q = iu.queries((len(LENS), q_len, 64, 128), 86)
+    if q_dtype:
+        q = q.to(torch.float8_e4m3fn).view(torch.uint8)
+    step = ops.DecodeStepEx(len(LENS), kv, wl.max_blocks, q_len=q_len, q_dtype=q_dtype, fused=fused)
+    args = (wl.cache, wl.kv_scale, wl.block_table, wl.seq_lens)
+    want = _run(step, q, *args)
+    assert _several(step, 0) > 1
+    bad = torch.zeros(want.shape[:3], dtype=torch.bool, device="cuda")
+    for s in (0, 1, 2, 5):
+        q[s, q_len - 1, 5, 77] = 0x7F if q_dtype else float("nan")
+        q[s, q_len - 1, 62, 0] = 0xFF if q_dtype else float("-inf" if s else "inf")
+        bad[s, q_len - 1, 5] = bad[s, q_len - 1, 62] = True
+    got = _run(step, q, *args)
+    assert bool(torch.isnan(got[bad]).all()), "a row that is not finite reads as %s" % got[bad][:, 0].tolist()
+    # (the other rows in bf16: how many items a merge takes at a time depends on
+    # which queue makes it, so the last bit of an fp32 sum may differ)
+    assert torch.allclose(got[~bad].float(), want[~bad].float(), rtol=2.0 ** -7, atol=0)
