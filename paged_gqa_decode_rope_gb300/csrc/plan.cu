@@ -158,7 +158,7 @@ extern "C" int hpc_decode_plan_ex(const int32_t* seq_lens, int32_t batch, int32_
   HPC_CHECK_ARG(min_tiles >= 1 && pool_chunks >= 0 && pool_chunks <= 64 && pp.pool_min_tiles >= 1);
   if (plan->num_ctas > HPC_MAX_PLAN_CTAS) return HPC_ERR_UNSUPPORTED;
   const size_t smem = sizeof(int) * hpc::plan_smem_ints(batch, plan->num_ctas);
-  const bool wide = smem > 48 * 1024 - 256;   // (the scans' static words included)
+  const bool wide = hpc::plan_smem_wide(smem);
   if (wide && hpc::plan_smem_optin() != cudaSuccess) return HPC_ERR_CUDA;
   auto launch = [&](auto kernel, int threads) {
     kernel<<<1, threads, smem, stream>>>(seq_lens, batch, max_blocks, min_tiles, pool_chunks, pp.pool_min_tiles,

@@ -158,6 +158,10 @@ __host__ __device__ __forceinline__ size_t plan_smem_ints(int batch, int num_cta
   return static_cast<size_t>(batch) + 1 + 2 * static_cast<size_t>(num_ctas) + 1;
 }
 
+// Whether that many dynamic bytes, with the scans' static words, pass the 48 KB
+// a kernel has without the opt-in.
+inline bool plan_smem_wide(size_t bytes) { return bytes > 48 * 1024 - 256; }
+
 // Items of one (seq, kv_head) segment: flat tiles [s0, s0 + n) cut at piece
 // starts.  Item j (global index first + j) is piece id(s0) + j clipped to the
 // segment.  An item that begins on a piece start records the CTA bounds that

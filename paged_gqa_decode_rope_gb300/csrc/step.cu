@@ -125,9 +125,8 @@ extern "C" int hpc_decode_step(const void* q, const void* k, const void* v,
         plan->seg_ptr, plan->home_end, plan->pool, plan->seg_done, plan->capacity, plan->num_ctas,
         status);
   };
-  // (beyond 48 KB the planner's arrays need the opt-in, once per device)
   auto run = [&](auto kernel, cudaError_t (*optin)()) {
-    if (smem > 48 * 1024 && optin() != cudaSuccess) return false;
+    if (hpc::plan_smem_wide(smem) && optin() != cudaSuccess) return false;
     args(kernel);
     return true;
   };

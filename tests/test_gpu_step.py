@@ -6,6 +6,7 @@ import pytest
 import torch
 
 from oracle import decode as od
+from paged_gqa_decode_rope_gb300 import workloads
 import gpu_util as gu
 
 pytestmark = pytest.mark.gpu
@@ -100,3 +101,35 @@ def test_decode_step_in_cuda_graph(two_launch):
     torch.cuda.synchronize()
     assert int(step.status.item()) == 0
     assert torch.equal(out, eager)
+
+
+@pytest.mark.parametrize("kv", [0, 1, 2])
+def test_step_whose_planner_just_fits_default_shared_memory(kv):
+    """8190 sequences on 2048 queues: the planner's arrays are 48 KB to the byte,
+    its scans' words come on top."""
+    import int4_util as iu
+    from paged_gqa_decode_rope_gb300 import ops
+    lens = np.zeros(8190, dtype=np.int32)
+    lens[[0, 1, 77, 4000, 8189]] = [300, 64, 1, 5000, 65]
+    if kv == 2:
+        wl = iu.Int4Batch(lens, 3)
+        scale, slots = None, workloads.slot_mapping_for(lens, wl.table)
+    else:
+        wl = workloads.Workload("custom", seed=3, lengths=lens, kv_dtype=kv)
+        scale, slots = wl.kv_scale, workloads.slot_mapping_for(lens, wl.block_table_np)
+    q, k, v = iu.queries((8190, 64, 128), 1), iu.queries((8190, 8, 128), 2), iu.queries((8190, 8, 128), 3)
+    w = torch.ones(128, dtype=torch.bfloat16, device="cuda")
+    pos = torch.as_tensor(np.maximum(lens - 1, 0), dtype=torch.int32, device="cuda")
+    cos_sin = ops.rope_cos_sin_cache(5000)
+    outs = []
+    for two in (True, False):
+        step = ops.DecodeStep(8190, kv, wl.max_blocks, n_ctas=2048)
+        cache = wl.cache.clone()
+        out = step(q, k, v, pos, cos_sin, w, w, cache, torch.as_tensor(slots, device="cuda"), scale, wl.block_table,
+                   wl.seq_lens, two_launch=two)
+        assert int(step.status.item()) == 0
+        outs.append((out.clone(), cache))
+    live = torch.as_tensor(lens > 0, device="cuda")
+    assert torch.equal(outs[0][1].view(torch.uint8), outs[1][1].view(torch.uint8))
+    assert bool((outs[0][0][live] != 0).any(-1).all()) and bool((outs[0][0][~live] == 0).all())
+    assert torch.allclose(outs[0][0].float(), outs[1][0].float(), rtol=2.0 ** -7, atol=0)
