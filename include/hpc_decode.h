@@ -618,7 +618,8 @@ int hpc_prefill_attn_staged(const void* q, int32_t num_tokens, const int32_t* qu
  *   slots    (device) int64 [num_slots], in any order, repeats allowed
  *   k_out, v_out  (device) [num_slots, 8, 128] of out_dtype, 16-byte aligned
  *   status   BAD_SLOT for a slot >= num_blocks * 64 (zeros)
- * Errors: HPC_ERR_INVALID_ARG for null pointers, num_blocks <= 0, num_slots < 0,
+ * Errors: HPC_ERR_INVALID_ARG for null pointers (slots, k_out and v_out may be
+ * null where num_slots is 0), num_blocks <= 0, num_slots < 0,
  * an E4M3 cache without kv_scale or a misaligned buffer; HPC_ERR_UNSUPPORTED
  * for an unknown dtype. */
 int hpc_kv_gather(const void* kv_cache, int32_t kv_dtype, const float* kv_scale, int32_t num_blocks,
@@ -658,7 +659,8 @@ int hpc_kv_gather(const void* kv_cache, int32_t kv_dtype, const float* kv_scale,
  *               id outside [0, num_blocks) in the table or the pool (its
  *               tokens get slot -1)
  * The outputs must not overlap the inputs (blocks read hist_lens and new_lens
- * while others write).  Errors: HPC_ERR_INVALID_ARG for null pointers, bad
+ * while others write).  Errors: HPC_ERR_INVALID_ARG for null pointers (an array
+ * of no entries, with batch or max_tokens 0, may be null), bad
  * sizes or seq_lens equal to hist_lens or new_lens; HPC_ERR_UNSUPPORTED for
  * batch > 8192, num_blocks > HPC_MAX_NUM_BLOCKS or batch * max_blocks >= 2^31. */
 int hpc_block_tables(const int32_t* hist_lens, const int32_t* new_lens, int32_t batch,

@@ -107,8 +107,8 @@ __global__ void __launch_bounds__(32 * kHkv) kv_gather_kernel(
 extern "C" int hpc_kv_gather(const void* kv_cache, int32_t kv_dtype, const float* kv_scale,
                              int32_t num_blocks, const int64_t* slots, int32_t num_slots, void* k_out,
                              void* v_out, int32_t out_dtype, int32_t* status, cudaStream_t stream) {
-  HPC_CHECK_ARG(kv_cache && slots && k_out && v_out && status);
   HPC_CHECK_ARG(num_blocks > 0 && num_slots >= 0);
+  HPC_CHECK_ARG(kv_cache && status && (num_slots == 0 || (slots && k_out && v_out)));
   if (kv_dtype != HPC_KV_BF16 && kv_dtype != HPC_KV_FP8_E4M3 && kv_dtype != HPC_KV_INT4)
     return HPC_ERR_UNSUPPORTED;
   if (out_dtype != HPC_OUT_BF16 && out_dtype != HPC_OUT_FP16 && out_dtype != HPC_OUT_FP32)

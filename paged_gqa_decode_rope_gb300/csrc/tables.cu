@@ -255,10 +255,11 @@ extern "C" int hpc_block_tables(const int32_t* hist_lens, const int32_t* new_len
                                 int32_t* block_table, int32_t max_blocks, int32_t* seq_lens,
                                 int32_t* query_start, int32_t* positions, int64_t* slot_mapping,
                                 int32_t max_tokens, int32_t* status, cudaStream_t stream) {
-  HPC_CHECK_ARG(hist_lens && new_lens && free_blocks && pool && block_table && seq_lens &&
-                query_start && positions && slot_mapping && status);
   HPC_CHECK_ARG(batch >= 0 && num_blocks > 0 && max_blocks >= 1 && max_tokens >= 0);
-  HPC_CHECK_ARG(seq_lens != hist_lens && seq_lens != new_lens);
+  HPC_CHECK_ARG(free_blocks && pool && query_start && status);
+  HPC_CHECK_ARG(batch == 0 || (hist_lens && new_lens && block_table && seq_lens && seq_lens != hist_lens &&
+                               seq_lens != new_lens));
+  HPC_CHECK_ARG(max_tokens == 0 || (positions && slot_mapping));
   if (batch > HPC_MAX_BATCH || num_blocks > HPC_MAX_NUM_BLOCKS) return HPC_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(batch) * max_blocks >= (int64_t{1} << 31) ||
       static_cast<int64_t>(max_blocks) * hpc::kPage >= (int64_t{1} << 31))
@@ -279,8 +280,8 @@ extern "C" int hpc_block_release(const int32_t* lens, const int32_t* keep_lens, 
                                  const int32_t* block_table, int32_t max_blocks, int32_t num_blocks,
                                  int32_t* free_blocks, int32_t* pool, int32_t* status,
                                  cudaStream_t stream) {
-  HPC_CHECK_ARG(lens && keep_lens && block_table && free_blocks && pool && status);
   HPC_CHECK_ARG(batch >= 0 && num_blocks > 0 && max_blocks >= 1);
+  HPC_CHECK_ARG(free_blocks && pool && status && (batch == 0 || (lens && keep_lens && block_table)));
   if (batch > HPC_MAX_BATCH || num_blocks > HPC_MAX_NUM_BLOCKS) return HPC_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(batch) * max_blocks >= (int64_t{1} << 31) ||
       static_cast<int64_t>(max_blocks) * hpc::kPage >= (int64_t{1} << 31))

@@ -269,3 +269,22 @@ def test_serving_run_over_the_4bit_cache():
     assert t.pool.tolist() == [40 - used, 0]
     for s in (status, t.status, pf.status, step.status, one.status):
         assert int(s.item()) == 0
+
+
+def test_calls_without_entries():
+    """No sequences, no tokens, no slots: nothing to do is no error."""
+    from paged_gqa_decode_rope_gb300 import ops
+    t, p = _pair(0, 4, 9, 5)                              # no sequences, all rows padding
+    want = p.step([], [])
+    t.step(_dev([]), _dev([]))
+    _same(t, p, want)
+    t.release(_dev([]), _dev([]))
+    _same(t, p, want)
+    t, p = _pair(3, 4, 9, 0)                              # no room for tokens
+    want = p.step([5, 0, 64], [0, 0, 0])
+    t.step(_dev([5, 0, 64]), _dev([0, 0, 0]))
+    _same(t, p, want)
+    for kv, cache in ((0, torch.zeros((2, 2, 8, 64, 128), dtype=torch.bfloat16, device="cuda")), (2, ops.int4_cache(2))):
+        k, v = (torch.empty((0, 8, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        ops.kv_gather(cache, kv, None, torch.empty(0, dtype=torch.int64, device="cuda"), k, v, t.status)
+    assert int(t.status.item()) == 0

@@ -158,3 +158,11 @@ def test_refusals_of_the_step(lib):
         b = list(a)
         b[i] = v
         assert lib.hpc_decode_step(*b) == rc, (i, v)
+
+
+def test_arrays_without_entries_may_be_null(lib):
+    assert lib.hpc_kv_gather(P, 2, None, 4, None, 0, None, None, 0, P, None) == 0
+    assert lib.hpc_block_release(None, None, 0, None, 8, 100, P, P, P, None) == 0
+    assert lib.hpc_kv_gather(P, 2, None, 4, None, 1, P, P, 0, P, None) == BAD
+    assert lib.hpc_block_tables(None, None, 0, 100, P, P, None, 8, None, P, None, None, 1, P, None) == BAD
+    assert lib.hpc_block_tables(None, P, 1, 100, P, P, P, 8, P, P, None, None, 0, P, None) == BAD
