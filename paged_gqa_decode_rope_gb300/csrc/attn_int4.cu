@@ -112,17 +112,15 @@ enum : int {
 // operands to F16 first, at a quarter of the rate.)
 //
 // The softmax takes maxima of scores before their scale, which is therefore
-// made positive: a negative sm_scale turns q's sign, zero makes q zero.
+// not negative (the calls refuse it); a scale of zero makes q zero.
 
 // Scale of a row of q whose largest magnitude has these bits, and what takes
 // scores of codes back to log2 units (NaN for a q with an infinity or a NaN).
 __device__ __forceinline__ void i4_row_scale(uint32_t am, float scale_log2, float& sc, float& back) {
   const int e2 = static_cast<int>(am >> 23) - 127;
   const int se = 4 - max(e2, -100);   // in [-124, 104]
-  sc = __uint_as_float(static_cast<uint32_t>(127 + se) << 23) *
-       (scale_log2 > 0.f ? 1.f : scale_log2 < 0.f ? -1.f : 0.f);
-  back = __uint_as_float(static_cast<uint32_t>(127 - se) << 23) * fabsf(scale_log2) * 0x1p24f;
-  if (scale_log2 == 0.f) back = 1.f;
+  sc = scale_log2 > 0.f ? __uint_as_float(static_cast<uint32_t>(127 + se) << 23) : 0.f;
+  back = scale_log2 > 0.f ? __uint_as_float(static_cast<uint32_t>(127 - se) << 23) * scale_log2 * 0x1p24f : 1.f;
   if (am >= 0x7f800000u) back = __uint_as_float(0x7fc00000u);
 }
 
@@ -1287,7 +1285,7 @@ template <int kNq>
 int launch_i4(const void* q, const void* kv_cache, int32_t num_blocks, const int32_t* block_table,
               int32_t max_blocks, const int32_t* seq_lens, int32_t batch, const hpc_attn_options& opts,
               const hpc_plan* plan, float* partial_o, float* partial_lse, float sm_scale, int32_t* status,
-              unsigned long long* cta_clock, void* out, bool pdl, cudaStream_t stream) {
+              unsigned long long* cta_clock, void* out, cudaStream_t stream) {
   using C = I4Cfg<kNq>;
   // once per device: the dynamic shared memory opt-in is a per-device setting
   static std::mutex mu;
@@ -1315,7 +1313,6 @@ int launch_i4(const void* q, const void* kv_cache, int32_t num_blocks, const int
   // Always a programmatic dependent: the kernel touches nothing global before
   // its wait for the previous kernel, whatever that is (the planner lets it
   // start at once: barriers and tensor memory are set up meanwhile).
-  (void)pdl;
   cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(
       &cfg, decode_attn_i4_kernel<kNq>, static_cast<const uint8_t*>(kv_cache),
@@ -1333,9 +1330,10 @@ int launch_i4(const void* q, const void* kv_cache, int32_t num_blocks, const int
 int hpc::launch_decode_attn_i4(HPC_LAYOUT_LAUNCH_ARGS) {
   (void)kv_dtype;
   (void)kv_scale;
+  (void)pdl;   // (it always is one)
   auto run = [&](auto launch) {
     return launch(q, kv_cache, num_blocks, block_table, max_blocks, seq_lens, batch, opts, plan, partial_o,
-                  partial_lse, sm_scale, status, cta_clock, out, pdl, stream);
+                  partial_lse, sm_scale, status, cta_clock, out, stream);
   };
   return opts.q_len == 1 ? run(hpc::launch_i4<1>) : opts.q_len == 2 ? run(hpc::launch_i4<2>) : run(hpc::launch_i4<4>);
 }
