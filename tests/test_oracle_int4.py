@@ -166,3 +166,32 @@ def test_arrays_without_entries_may_be_null(lib):
     assert lib.hpc_kv_gather(P, 2, None, 4, None, 1, P, P, 0, P, None) == BAD
     assert lib.hpc_block_tables(None, None, 0, 100, P, P, None, 8, None, P, None, None, 1, P, None) == BAD
     assert lib.hpc_block_tables(None, P, 1, 100, P, P, P, 8, P, P, None, None, 0, P, None) == BAD
+
+
+def test_bound_of_one_rounding_tells_one_from_two():
+    """The bound that the decode attention is held to: P times the scale rounded
+    to bf16 once, from fp32 or from P as a sum of two bf16, keeps it; rounding P
+    first and the product again does not."""
+    import int4_util as iu
+    b = iu.Int4Batch([2, 3] * 20, 7, device=None)
+    r = np.random.default_rng(8)
+    worst = {"once": 0.0, "sum": 0.0, "twice": 0.0}
+    bf = nx.bf16_round
+    for s, L in enumerate(b.lengths):
+        for h in range(8):
+            n = -(-int(L) // 64)
+            K, V = b.rows(s, h)
+            q = bf(r.standard_normal(128))
+            want, size = iu.attention(q, K, V, int(L))
+            x = K @ q / np.sqrt(128)
+            p = np.exp(x - x.max())[:, None]
+            rec = b.host[b.table[s, :n], h]
+            bits = rec[:, oi._SCALE[1]].astype(np.uint16) | (rec[:, oi._SCALE[1] + 1].astype(np.uint16) << 8)
+            sc = np.repeat(nx.bf16_from_bits(bits).reshape(-1, 4)[:L], 32, axis=-1)
+            codes = np.rint(V / sc)
+            hi = bf(p)
+            w = {"once": bf(p * sc), "sum": bf(hi * sc + bf(bf(p - hi) * sc)), "twice": bf(hi * sc)}
+            for k, x in w.items():
+                err = np.abs((x * codes).sum(0) / p.sum() - want)
+                worst[k] = max(worst[k], float((err / (iu.WEIGHT_ONCE * size + 1e-30)).max()))
+    assert worst["once"] < 1 and worst["sum"] < 1 < worst["twice"], worst
