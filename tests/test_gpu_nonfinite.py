@@ -106,3 +106,29 @@ def test_query_that_is_not_finite(kv, q_dtype, q_len, fused):
     # (the other rows in bf16: how many items a merge takes at a time depends on
     # which queue makes it, so the last bit of an fp32 sum may differ)
     assert torch.allclose(got[~bad].float(), want[~bad].float(), rtol=2.0 ** -7, atol=0)
+
+
+@pytest.mark.parametrize("kv,staged", [(0, False), (1, False), (1, True), (2, True)])
+def test_prefill_query_that_is_not_finite(kv, staged):
+    from paged_gqa_decode_rope_gb300 import ops
+    from paged_gqa_decode_rope_gb300.workloads import Workload
+    lens, new = [700, 64, 300], [200, 64, 1]
+    wl = iu.Int4Batch(lens, 87) if kv == INT4 else \
+        Workload("custom", seed=87, lengths=lens, kv_dtype=kv, include_new_token=True)
+    q = iu.queries((265, 64, 128), 88)
+    qst = torch.tensor([0, 200, 264, 265], dtype=torch.int32, device="cuda")
+    pf = ops.PrefillAttention(3, out_dtype=ops.OUT_FP32,
+                              staging_pages=ops.PrefillAttention.pages_for(lens) if staged else 0)
+    outs = []
+    bad = torch.zeros((265, 64), dtype=torch.bool, device="cuda")
+    for k in range(2):
+        pf.plan(qst)
+        outs.append(pf(q, qst, wl.cache, kv, None if kv == INT4 else wl.kv_scale, wl.block_table, wl.seq_lens,
+                       torch.full((265, 64, 128), 7.0, device="cuda")))
+        assert int(pf.status.item()) == 0
+        for i in (0, 130, 199, 230, 264):
+            q[i, 5, 77] = float("nan")
+            q[i, 62, 0] = float("-inf" if i % 2 else "inf")
+            bad[i, 5] = bad[i, 62] = True
+    assert bool(torch.isnan(outs[1][bad]).all()), outs[1][bad][:, 0].tolist()
+    assert torch.equal(outs[1][~bad], outs[0][~bad])
