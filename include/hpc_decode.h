@@ -586,11 +586,15 @@ int hpc_prefill_attn(const void* q, int32_t num_tokens, const int32_t* query_sta
  * scales.  Three launches: the page prefix, the conversion, the attention.
  * The result is the attention over the dequantised cache, with P stored as
  * BF16 (as for a BF16 cache) instead of F16.  A 4-bit cache's values (code
- * times scale, 12 significant bits) are staged rounded to BF16, their scales
- * multiplied in.  For a BF16 cache this is hpc_prefill_attn (staging unused).
+ * times scale, 11 significant bits) are staged as F16, exactly, times a power
+ * of two per page and head that the kernel takes back, and q and P are F16 in
+ * the products: the only roundings are P's (2^-11) and the output's.  (Exact for
+ * scales down to 2^-13 of the page's largest and above 2^-106, and for elements
+ * of q down to 2^-25 of their row's largest.)  For a BF16 cache this is
+ * hpc_prefill_attn (staging unused).
  * Source: as hpc_prefill_attn.
  * Arguments as hpc_prefill_attn, and:
- *   staging        (device) [staging_pages][2][8][64][128] bf16, 16-byte
+ *   staging        (device) [staging_pages][2][8][64][128] of 16 bits, 16-byte
  *                  aligned, written: staged page page_ptr[b] + j holds block
  *                  block_table[b][j] of sequence b
  *   staging_pages  pages staging holds; it needs sum_b ceil(seq_lens[b] / 64)

@@ -133,17 +133,17 @@ __global__ void __launch_bounds__(kStageThreads) stage_convert_kernel(
   }
 }
 
-// Every record the batch reads, 4-bit codes -> BF16 (code times scale, rounded
-// once: relative error at most 2^-8, as of a value stored in a BF16 cache),
-// into the same staged pages.  A block takes one (page, KV head) record at a
-// time: the 9 KB land in shared memory coalesced, then every thread writes 16
-// bytes of a staged row a step (rows are read out of the record's fragment
-// order there, not from memory).  Bound by memory: the pages of 4 x 4096 tokens
+// Every record the batch reads, 4-bit codes -> F16 (code times scale, 11
+// significant bits, times the tile's power of two: see i4_tile_bin), into the
+// same staged pages.  A block takes one (page, KV head) record at a time: the 9 KB
+// land in shared memory coalesced, every warp takes the powers from the scales, then
+// every thread writes 16 bytes of a staged row a step (rows are read out of the
+// record's fragment order there, not from memory).  Bound by memory: the pages of 4 x 4096 tokens
 // 18 us, 86 MB in and out at 4.8 TB/s, before an attention of 722 us.
 __global__ void __launch_bounds__(kStageThreads) stage_convert_i4_kernel(
     const uint8_t* __restrict__ cache, int32_t num_blocks, const int32_t* __restrict__ block_table,
-    int32_t max_blocks, int32_t batch, const int32_t* __restrict__ page_ptr, int32_t staged_pages,
-    uint16_t* __restrict__ staged) {
+    int32_t max_blocks, const int32_t* __restrict__ seq_lens, int32_t batch,
+    const int32_t* __restrict__ page_ptr, int32_t staged_pages, uint16_t* __restrict__ staged) {
   __shared__ __align__(16) uint8_t rec[kI4Record];
   const int64_t total = static_cast<int64_t>(min(page_ptr[batch], staged_pages)) * kHkv;
   for (int64_t u = blockIdx.x; u < total; u += gridDim.x) {
@@ -162,21 +162,27 @@ __global__ void __launch_bounds__(kStageThreads) stage_convert_i4_kernel(
     for (int z = threadIdx.x; z < kI4Record / 16; z += kStageThreads)
       reinterpret_cast<uint4*>(rec)[z] = src[z];
     __syncthreads();
+    const int lane = threadIdx.x & 31;
+    const int keep = seq_lens[lo] - kPage * (pg - page_ptr[lo]);
+    const float kp = pow2(i4_bin_power(
+        i4_tile_bin<false>(*reinterpret_cast<const uint4*>(rec + kI4OffKs + 16 * lane), lane, keep)));
+    const float vp = pow2(i4_bin_power(
+        i4_tile_bin<true>(*reinterpret_cast<const uint4*>(rec + kI4OffVs + 16 * lane), lane, keep)));
     uint16_t* k_page = staged + (static_cast<int64_t>(pg) * 2 * kHkv + h) * kPage * kD;
     uint16_t* v_page = k_page + static_cast<int64_t>(kHkv) * kPage * kD;
 #pragma unroll
     for (int z = threadIdx.x; z < kPage * kD / 8; z += kStageThreads) {   // 8 elements of a row
       const int t = z / (kD / 8), d = (z % (kD / 8)) * 8, g = d / kI4Group;
       const uint32_t kw = *reinterpret_cast<const uint32_t*>(rec + i4_k_byte(t, d));
-      const float ks = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(rec + i4_ks_byte(t, g)));
+      const float ks = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(rec + i4_ks_byte(t, g))) * kp;
       const uint32_t vw = *reinterpret_cast<const uint16_t*>(rec + i4_v_byte(t, d)) |
                           (static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(rec + i4_v_byte(t, d + 4))) << 16);
-      const float vs = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(rec + i4_vs_byte(t, g)));
+      const float vs = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(rec + i4_vs_byte(t, g))) * vp;
       uint32_t ko[4], vo[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        ko[k] = pack_bf16(i4_value(kw, 2 * k, ks), i4_value(kw, 2 * k + 1, ks));
-        vo[k] = pack_bf16(i4_value(vw, 2 * k, vs), i4_value(vw, 2 * k + 1, vs));
+        ko[k] = pack_f16(i4_value(kw, 2 * k, ks), i4_value(kw, 2 * k + 1, ks));
+        vo[k] = pack_f16(i4_value(vw, 2 * k, vs), i4_value(vw, 2 * k + 1, vs));
       }
       *reinterpret_cast<uint4*>(k_page + t * kD + d) = make_uint4(ko[0], ko[1], ko[2], ko[3]);
       *reinterpret_cast<uint4*>(v_page + t * kD + d) = make_uint4(vo[0], vo[1], vo[2], vo[3]);
@@ -184,7 +190,7 @@ __global__ void __launch_bounds__(kStageThreads) stage_convert_i4_kernel(
   }
 }
 
-template <bool kFp8>
+template <int kForm>
 cudaError_t prefill_tc_smem_optin() {
   static std::mutex mu;
   static bool done[64] = {};
@@ -196,11 +202,11 @@ cudaError_t prefill_tc_smem_optin() {
   // the warpgroups' raised register budgets must fit what a CTA is launched
   // with, or the raise would wait for registers that never come
   cudaFuncAttributes fa;
-  e = cudaFuncGetAttributes(&fa, prefill_tc_kernel<kFp8>);
+  e = cudaFuncGetAttributes(&fa, prefill_tc_kernel<kForm>);
   if (e != cudaSuccess) return e;
-  if (fa.numRegs * tc::Cfg<kFp8>::kThreads < tc::regs_needed<kFp8>())
+  if (fa.numRegs * tc::Cfg<kForm>::kThreads < tc::regs_needed<kForm>())
     return cudaErrorInvalidConfiguration;
-  e = cudaFuncSetAttribute(prefill_tc_kernel<kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  e = cudaFuncSetAttribute(prefill_tc_kernel<kForm>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            tc::kSmemBytes);
   if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
   return e;
@@ -253,7 +259,7 @@ int prefill_run(const void* q, int32_t num_tokens, const int32_t* query_start, c
   if (batch == 0 || num_tokens == 0) return HPC_OK;
   auto encode = tensor_map_encoder();
   if (encode == nullptr) return HPC_ERR_CUDA;
-  // the pages the kernel streams: the cache, or its staged BF16 copy
+  // the pages the kernel streams: the cache, or its staged 16-bit copy
   const void* pages = staged ? staging : kv_cache;
   const bool pages_fp8 = fp8 && !staged;
   const int32_t map_blocks = staged ? staging_pages : num_blocks;
@@ -290,24 +296,36 @@ int prefill_run(const void* q, int32_t num_tokens, const int32_t* query_start, c
     return HPC_ERR_CUDA;
   if (staged) {
     stage_plan_kernel<<<1, kPfPlanThreads, 0, stream>>>(seq_lens, batch, max_blocks, page_ptr, status);
-    (i4 ? stage_convert_i4_kernel : stage_convert_kernel)<<<8 * sms, kStageThreads, 0, stream>>>(
-        static_cast<const uint8_t*>(kv_cache), num_blocks, block_table, max_blocks, batch, page_ptr,
-        staging_pages, static_cast<uint16_t*>(staging));
+    if (i4)
+      stage_convert_i4_kernel<<<8 * sms, kStageThreads, 0, stream>>>(
+          static_cast<const uint8_t*>(kv_cache), num_blocks, block_table, max_blocks, seq_lens, batch, page_ptr,
+          staging_pages, static_cast<uint16_t*>(staging));
+    else
+      stage_convert_kernel<<<8 * sms, kStageThreads, 0, stream>>>(
+          static_cast<const uint8_t*>(kv_cache), num_blocks, block_table, max_blocks, batch, page_ptr,
+          staging_pages, static_cast<uint16_t*>(staging));
     if (cudaPeekAtLastError() != cudaSuccess) return HPC_ERR_CUDA;
   }
-  if (pages_fp8) {
-    if (prefill_tc_smem_optin<true>() != cudaSuccess) return HPC_ERR_CUDA;
-    prefill_tc_kernel<true><<<sms, tc::Cfg<true>::kThreads, tc::kSmemBytes, stream>>>(
+  if (i4) {
+    // F16 pages, their powers of two from the records' scales
+    if (prefill_tc_smem_optin<tc::kStaged16>() != cudaSuccess) return HPC_ERR_CUDA;
+    prefill_tc_kernel<tc::kStaged16><<<sms, tc::Cfg<tc::kStaged16>::kThreads, tc::kSmemBytes, stream>>>(
+        map, q_map, num_tokens, static_cast<const uint8_t*>(kv_cache), nullptr, query_start, seq_lens, batch,
+        block_table, max_blocks, num_blocks, unit_ptr, counters, out, out_dtype, sm_scale, status, page_ptr,
+        staging_pages);
+  } else if (pages_fp8) {
+    if (prefill_tc_smem_optin<tc::kE4m3Cache>() != cudaSuccess) return HPC_ERR_CUDA;
+    prefill_tc_kernel<tc::kE4m3Cache><<<sms, tc::Cfg<tc::kE4m3Cache>::kThreads, tc::kSmemBytes, stream>>>(
         map, q_map, num_tokens, static_cast<const uint8_t*>(kv_cache), kv_scale, query_start,
         seq_lens, batch, block_table, max_blocks, num_blocks, unit_ptr, counters, out, out_dtype,
         sm_scale, status, nullptr, 0);
   } else {
     // BF16 pages: the cache itself (no scales, whatever kv_scale points at),
     // or the staged copy of an E4M3 cache (its scales; the real block table
-    // still says which tiles are bad) or of a 4-bit one (scales multiplied in)
-    if (prefill_tc_smem_optin<false>() != cudaSuccess) return HPC_ERR_CUDA;
-    prefill_tc_kernel<false><<<sms, tc::Cfg<false>::kThreads, tc::kSmemBytes, stream>>>(
-        map, q_map, num_tokens, static_cast<const uint8_t*>(pages), staged && fp8 ? kv_scale : nullptr,
+    // still says which tiles are bad)
+    if (prefill_tc_smem_optin<tc::kBf16Pages>() != cudaSuccess) return HPC_ERR_CUDA;
+    prefill_tc_kernel<tc::kBf16Pages><<<sms, tc::Cfg<tc::kBf16Pages>::kThreads, tc::kSmemBytes, stream>>>(
+        map, q_map, num_tokens, static_cast<const uint8_t*>(pages), staged ? kv_scale : nullptr,
         query_start, seq_lens, batch, block_table, max_blocks, num_blocks, unit_ptr, counters, out,
         out_dtype, sm_scale, status, staged ? page_ptr : nullptr, staged ? staging_pages : 0);
   }

@@ -37,9 +37,26 @@
 // F16 operands.  The K
 // scale joins the softmax scale and the V scale the final division, so the
 // result is the attention over the dequantised cache.
+//
+// 4-bit caches (kStaged16): pages staged as F16, exactly, times a power of two per
+// tile (i4_tile_bin), and Q turned into F16 times one per row by the softmax warps.
+// So no operand is rounded, and P keeps F16's 11 bits.  (K, V and P as BF16: errors
+// of 0.0031 of the outputs' size, against 0.0016 of their own rounding alone; V and
+// P as F16, K as BF16: 0.0026.)  Q costs 2 us a unit of 26, as the next unit's first
+// product waits for it: done while the last P V runs it delays the output more (13
+// us of 800 in all), and a warpgroup for it takes registers from the softmax (40).  The powers change with their bin only, hardly ever between the tiles
+// of one head.  The row's and K's join the softmax scale.  With V's exponent ev,
+// the running maximum is one of products, max(score + ev), kept less ev: P =
+// 2^(score - maximum + 7) is at most 2^15, exact to 2^-11 down to 2^-14 and in steps
+// of 2^-24 below.  Where ev has changed within a unit, the row sum keeps a reference
+// of its own, and a tile whose products stay 2^-40 below the largest adds nothing to
+// O: its P is zero, and its part of the row sum is taken by its own maximum, as P
+// could underflow there.
 #pragma once
 
-#include "common.cuh"
+#include <type_traits>
+
+#include "int4.cuh"
 
 namespace hpc {
 namespace {
@@ -59,10 +76,11 @@ constexpr int kTileBytes = 2 * kPage;               // K + V of one tile as the 
 constexpr int kQBytes = 2 * 128 * 128;              // per lane: 2 halves of d x 128 rows x 128 B
 constexpr int kOffBar = 208 * 1024;                 // after the rings and Q of either layout
 
-template <bool kFp8>
+enum Form { kBf16Pages = 0, kE4m3Cache = 1, kStaged16 = 2 };
+template <int kForm>
 struct Cfg;
 template <>
-struct Cfg<false> {   // BF16 cache: the MMA reads the TMA ring itself
+struct Cfg<kBf16Pages> {   // BF16 cache: the MMA reads the TMA ring itself
   static constexpr int kThreads = 384;
   static constexpr int kPStages = 4;                // producer ring (TMA)
   static constexpr int kPStageBytes = 2 * kPage;    // K page + V page
@@ -73,7 +91,7 @@ struct Cfg<false> {   // BF16 cache: the MMA reads the TMA ring itself
   static constexpr int kUnitReaders = 11;           // 2 MMA, Q loader, 8 softmax warps
 };
 template <>
-struct Cfg<true> {    // E4M3 cache: the converter reads the codes itself into F16 tiles
+struct Cfg<kE4m3Cache> {   // E4M3 cache: the converter reads the codes itself into F16 tiles
   static constexpr int kThreads = 512;
   static constexpr int kPStages = 4;                // (no TMA ring: the producer loads no tile)
   static constexpr int kPStageBytes = 0;
@@ -83,14 +101,16 @@ struct Cfg<true> {    // E4M3 cache: the converter reads the codes itself into F
   static constexpr uint32_t kRegsSoftmax = 176, kRegsMid = 64, kRegsConv = 96;
   static constexpr int kUnitReaders = 15;           // + the 4 converter warps
 };
-static_assert(Cfg<false>::kOffQ + 2 * kQBytes <= kOffBar, "BF16 layout overlaps the barriers");
-static_assert(Cfg<true>::kOffQ + 2 * kQBytes <= kOffBar, "E4M3 layout overlaps the barriers");
-static_assert(Cfg<false>::kPStages <= 4 && Cfg<true>::kPStages <= 4 && Cfg<true>::kMStages <= 4,
+template <>
+struct Cfg<kStaged16> : Cfg<kBf16Pages> {};
+static_assert(Cfg<kBf16Pages>::kOffQ + 2 * kQBytes <= kOffBar, "BF16 layout overlaps the barriers");
+static_assert(Cfg<kE4m3Cache>::kOffQ + 2 * kQBytes <= kOffBar, "E4M3 layout overlaps the barriers");
+static_assert(Cfg<kBf16Pages>::kPStages <= 4 && Cfg<kE4m3Cache>::kPStages <= 4 && Cfg<kE4m3Cache>::kMStages <= 4,
               "barrier and flag arrays hold four stages");
 
-template <bool kFp8>
+template <int kForm>
 constexpr int regs_needed() {   // per CTA, for the warpgroups' raised budgets
-  return 256 * Cfg<kFp8>::kRegsSoftmax + 128 * Cfg<kFp8>::kRegsMid + 128 * Cfg<kFp8>::kRegsConv;
+  return 256 * Cfg<kForm>::kRegsSoftmax + 128 * Cfg<kForm>::kRegsMid + 128 * Cfg<kForm>::kRegsConv;
 }
 
 // mbarriers (index of the first of each kind; [l] per lane, [l][i] per lane and buffer)
@@ -104,7 +124,7 @@ constexpr int kBarPFull = 24;      // [2][2] P written over the scores (128 soft
 constexpr int kBarOFinal = 28;     // [2] the lane's last P V of a unit done
 constexpr int kBarOFree = 30;      // [2] the lane's O read out (128 softmax threads)
 constexpr int kBarQFull = 32;      // [2] the lane's Q tile landed (TMA)
-constexpr int kBarQReady = 34;     // [2] E4M3: the lane's Q tile turned into F16 (128 threads)
+constexpr int kBarQReady = 34;     // [2] E4M3, 4-bit: the lane's Q tile turned into F16 (128 threads)
 constexpr int kBarQFree = 36;      // [2] the lane's last Q K^T of a unit done
 constexpr int kBarUnitFull = 38;   // [2] unit descriptor handed on
 constexpr int kBarUnitEmpty = 40;  // [2] unit descriptor read (every warp that follows units)
@@ -124,6 +144,9 @@ constexpr uint32_t kTmemCols = 512;                 // lane l: S 256l + {0, 64},
 constexpr int kLaneTokens = 16;
 constexpr int kUnitTokens = 32;
 constexpr float kRescaleLog2 = 8.0f;                // rescale O only when the max grows by > 2^8
+constexpr float kLiftLog2 = 7.0f;                   // 4-bit: P times 2^7, so at most 2^15
+constexpr float kFarLog2 = 40.0f;                   // 4-bit: a tile this far below adds nothing
+constexpr int kMarkBias = 16;                       // 4-bit: a good tile's mark holds the bins of K and V + 16
 
 // tiles of a lane of a unit: 0 without new tokens, else those its last token sees
 __device__ __forceinline__ int lane_tiles(int qlen, int L, int first_token) {
@@ -182,8 +205,8 @@ __device__ __forceinline__ void umma_qk_lane(uint32_t d, uint64_t q, uint64_t k,
 #undef HPC_QK_STEP
 }
 
-template <bool kFp8>
-__global__ void __launch_bounds__(tc::Cfg<kFp8>::kThreads, 1) prefill_tc_kernel(
+template <int kForm>
+__global__ void __launch_bounds__(tc::Cfg<kForm>::kThreads, 1) prefill_tc_kernel(
     const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap q_map,
     int32_t num_tokens, const uint8_t* __restrict__ kv_codes, const float* __restrict__ kv_scale,
     const int32_t* __restrict__ query_start, const int32_t* __restrict__ seq_lens, int32_t batch,
@@ -191,15 +214,17 @@ __global__ void __launch_bounds__(tc::Cfg<kFp8>::kThreads, 1) prefill_tc_kernel(
     const int32_t* __restrict__ unit_ptr, int32_t* counters, void* __restrict__ out,
     int32_t out_dtype, float sm_scale, int32_t* __restrict__ status,
     const int32_t* __restrict__ page_ptr, int32_t staged_pages) {
+  constexpr bool kFp8 = kForm == tc::kE4m3Cache, k16 = kForm == tc::kStaged16;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + tc::kOffBar);
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
   volatile int* ring = reinterpret_cast<volatile int*>(smem + tc::kOffRing);
-  using C = tc::Cfg<kFp8>;
+  using C = tc::Cfg<kForm>;
   // per producer stage and per tile the MMA side holds: 1 = a good block
   volatile int* stage_ok = reinterpret_cast<volatile int*>(smem + tc::kOffOk);
+  // (4-bit: the bins of K and V)
   volatile int* tile_ok_of = kFp8 ? stage_ok + 4 : stage_ok;
   // the MMA side's ring: the TMA stages themselves, or the F16 tiles
   constexpr int kBarTileFull = kFp8 ? tc::kBarMFull : tc::kBarRawFull;
@@ -342,9 +367,28 @@ __global__ void __launch_bounds__(tc::Cfg<kFp8>::kThreads, 1) prefill_tc_kernel(
         const int t = tb + lane;
         const int bids = t < ntiles ? block_table[static_cast<int64_t>(b) * max_blocks + t] : 0;
         const int page0 = page_ptr != nullptr ? page_ptr[b] + tb : 0;   // staged page of tile tb
-        for (int jj = 0; jj < min(32, ntiles - tb) && alive; ++jj) {
+        // 4-bit: the scales of a tile's record, loaded a tile ahead
+        const int L = k16 ? seq_lens[b] : 0;
+        uint4 ks = make_uint4(0u, 0u, 0u, 0u), vs = ks;
+        auto load_scales = [&](int jj) {
+          const int bid = __shfl_sync(0xffffffffu, bids, jj);
+          if (bid < 0 || bid >= num_blocks) return;
+          const uint8_t* sc = kv_codes + (static_cast<int64_t>(bid) * kHkv + h) * kI4Record + kI4OffKs + 16 * lane;
+          ks = *reinterpret_cast<const uint4*>(sc);
+          vs = *reinterpret_cast<const uint4*>(sc + (kI4OffVs - kI4OffKs));
+        };
+        const int in_chunk = min(32, ntiles - tb);
+        if (k16) load_scales(0);
+        for (int jj = 0; jj < in_chunk && alive; ++jj) {
           const int bid = __shfl_sync(0xffffffffu, bids, jj);
           const bool good = bid >= 0 && bid < num_blocks;
+          int mark = 1;
+          if (k16) {
+            const int keep = L - kPage * (tb + jj);
+            mark = (i4_tile_bin<false>(ks, lane, keep) + tc::kMarkBias) << 8 |
+                   (i4_tile_bin<true>(vs, lane, keep) + tc::kMarkBias);
+            if (jj + 1 < in_chunk) load_scales(jj + 1);
+          }
           const int s = static_cast<int>(g % C::kPStages);
           int tok = 1;
           if (lane == 0) {
@@ -362,7 +406,7 @@ __global__ void __launch_bounds__(tc::Cfg<kFp8>::kThreads, 1) prefill_tc_kernel(
               }
             }
             if (tok && good) {
-              stage_ok[s] = 1;
+              stage_ok[s] = mark;
               const uint32_t fb = bar(tc::kBarRawFull + s);
               mbar_arrive_expect_tx(fb, C::kPStageBytes);
               const uint32_t dst = base + s * C::kPStageBytes;
@@ -419,15 +463,15 @@ __global__ void __launch_bounds__(tc::Cfg<kFp8>::kThreads, 1) prefill_tc_kernel(
     // and each commit.
     regs_dec<C::kRegsMid>();
     const int l = warp == tc::kWarpMma ? 0 : 1;
-    constexpr uint32_t kIdescS = kFp8 ? umma_idesc_f16(128, 64, false) : umma_idesc_bf16(128, 64, false);
-    constexpr uint32_t kIdescO = kFp8 ? umma_idesc_f16(128, 128, true) : umma_idesc_bf16(128, 128, true);
+    constexpr uint32_t kIdescS = kFp8 || k16 ? umma_idesc_f16(128, 64, false) : umma_idesc_bf16(128, 64, false);
+    constexpr uint32_t kIdescO = kFp8 || k16 ? umma_idesc_f16(128, 128, true) : umma_idesc_bf16(128, 128, true);
     // descriptors of the first step of each operand; a step adds a constant
     const uint64_t desc_q = umma_smem_desc(base + C::kOffQ + l * tc::kQBytes, 1024, 1024);
     const uint64_t desc_k = umma_smem_desc(base + C::kOffM, 1024, 1024);
     const uint64_t desc_v = umma_smem_desc(base + C::kOffM + tc::kPage, tc::kBox, 1024);
     constexpr uint64_t kStageStep = tc::kTileBytes >> 4;
     const uint32_t tl = tmem + 256 * l;   // the lane's columns: S 0 / 64, O 128
-    constexpr int kBarQ = kFp8 ? tc::kBarQReady : tc::kBarQFull;   // Q as the MMA reads it
+    constexpr int kBarQ = kFp8 || k16 ? tc::kBarQReady : tc::kBarQFull;   // Q as the MMA reads it
     uint32_t G = 0, U = 0, Gl = 0, Vl = 0;   // stream tiles, units read, lane tiles, lane units
     bool dead = false;
     Unit d;
@@ -515,12 +559,51 @@ __global__ void __launch_bounds__(tc::Cfg<kFp8>::kThreads, 1) prefill_tc_kernel(
     const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 256 * l;
     // E4M3: scores of the codes times the K scale, outputs times the V scale
     // (also for BF16 pages staged from an E4M3 cache: the host passes the scales then)
-    const float scale_log2 =
+    const float scale_all =
         sm_scale * 1.4426950408889634f * (kFp8 || kv_scale != nullptr ? kv_scale[0] : 1.f);
     const float v_scale = kFp8 || kv_scale != nullptr ? kv_scale[1] : 1.f;
     uint32_t G = 0, U = 0, Gl = 0, Vl = 0;
     bool dead = false;
     Unit d;
+    // 4-bit: the lane's Q tile of the unit from BF16 to F16 in place, thread = row,
+    // times the power of two that puts the row's largest element in [2^11, 2^12):
+    // exact for elements down to 2^-25 of it, within 2^-26 of it below.  c_row
+    // takes its scores back; it is NaN for a row with an infinity or a NaN.
+    float c_row = scale_all;
+    auto take_q = [&]() -> bool {
+      if (!wait_all(tc::kBarQFull + l, Vl & 1)) return false;
+      uint8_t* qrow = smem + C::kOffQ + l * tc::kQBytes + row * 128;
+      // (chunk order rotated by the row, as below for E4M3 caches)
+      auto chunk = [&](int k) {
+        const int cc = (k & 8) | ((k ^ row) & 7);
+        return reinterpret_cast<uint4*>(qrow + (cc >> 3) * 2 * tc::kBox + (cc & 7) * 16);
+      };
+      uint4 w[16];
+      uint32_t top = 0;   // (a NaN's bits are the largest)
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        w[k] = *chunk(k);
+        const uint32_t m = __vmaxu2(__vmaxu2(w[k].x & 0x7fff7fffu, w[k].y & 0x7fff7fffu),
+                                    __vmaxu2(w[k].z & 0x7fff7fffu, w[k].w & 0x7fff7fffu));
+        top = __vmaxu2(top, m);
+      }
+      top = max(top & 0xffffu, top >> 16);
+      const int up = 11 - max(static_cast<int>(top >> 7) - 127, -100);   // in -117 .. 111
+      // on the bits, two at a time: the exponent less the biases' difference and the
+      // power, and three places up
+      const uint32_t least = static_cast<uint32_t>(127 - 15 - up) << 7;
+      const uint32_t least2 = least | least << 16;
+      auto turn = [&](uint32_t x) {
+        return ((__vmaxu2(x & 0x7fff7fffu, least2) - least2) << 3) | (x & 0x80008000u);
+      };
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        *chunk(k) = make_uint4(turn(w[k].x), turn(w[k].y), turn(w[k].z), turn(w[k].w));
+      c_row = top >= 0x7f80u ? __uint_as_float(0x7fc00000u) : scale_all * pow2(-up);
+      fence_proxy_async_smem();
+      mbar_arrive(bar(tc::kBarQReady + l));
+      return true;
+    };
     while (!dead) {
       if (!read_unit(U, d)) break;
       ++U;
@@ -538,102 +621,166 @@ __global__ void __launch_bounds__(tc::Cfg<kFp8>::kThreads, 1) prefill_tc_kernel(
       const int pos = L - qlen + i;
       const int head = d.h * kGroup + hl;
       float m_used = -INFINITY, lsum = 0.f;
-      for (int j = 0; j < ntl; ++j) {
-        const uint32_t g = G + j, gl = Gl + j;
-        const int s = static_cast<int>(g % C::kMStages);
-        if (!wait_all(tc::kBarSFull + 2 * l + (gl & 1), (gl >> 1) & 1) ||
-            !wait_all(kBarTileFull + s, (g / C::kMStages) & 1)) {
-          dead = true;
-          break;
+      float scale_log2 = scale_all;
+      // 4-bit: the bins' mark and V's exponent; once that has changed (shifted),
+      // the row sum's reference
+      int cur = 0, ev = 0;
+      bool shifted = false;
+      float sum_ref = 0.f;
+      auto rebin = [&](int mark) {
+        const int e = -i4_bin_power((mark & 0xff) - tc::kMarkBias);
+        // (positive, as masked scores are -inf)
+        scale_log2 = max_nan(c_row * pow2(-i4_bin_power((mark >> 8) - tc::kMarkBias)), 0x1p-126f);
+        if (cur != 0 && e != ev) {
+          if (!shifted) sum_ref = m_used;
+          shifted = true;
+          m_used += static_cast<float>(ev - e);
         }
-        tc_fence_after();
-        uint32_t sr[64];
-        tmem_ld64(trow + 64 * (gl & 1), sr);
-        tmem_wait_ld();
-        const bool tile_ok = tile_ok_of[s] != 0;
-        const int key0 = j * kPage;
-        // keys of this tile the row sees: 0 .. lim (none for lim < 0); only
-        // the tiles on a row's diagonal (or a bad tile) need the mask, which
-        // sets the other scores to -inf in place (a copy of the row would
-        // cost a move per score on the unmasked tiles)
-        const int lim = (valid && tile_ok) ? min(63, pos - key0) : -1;
-        if (!__all_sync(0xffffffffu, lim == 63)) {
-#pragma unroll
-          for (int jk = 0; jk < 64; ++jk)
-            if (jk > lim) sr[jk] = 0xff800000u;
-        }
-        // the row maximum of the raw scores, three-input maxima in 8
-        // independent chains (each started from a pair); the scale is
-        // positive, so it commutes with the maximum
-        float m8[8];
-#pragma unroll
-        for (int jk = 0; jk < 64; jk += 2) {
-          const int c = (jk >> 1) & 7;
-          const float a = __uint_as_float(sr[jk]), b = __uint_as_float(sr[jk + 1]);
-          m8[c] = jk < 16 ? fmaxf(a, b) : max3f(m8[c], a, b);
-        }
-        const float mx =
-            max3f(max3f(m8[0], m8[1], m8[2]), max3f(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7])) *
-            scale_log2;
-        // the running maximum moves only when it grows by more than 2^8
-        // (weights stay <= 2^8); the row's O is then rescaled in TMEM
-        const bool grow = mx > m_used + tc::kRescaleLog2;
-        const float alpha = grow ? exp2_ftz(m_used - mx) : 1.f;   // 0 while m_used = -inf
-        if (grow) {
-          lsum *= alpha;
-          m_used = mx;
-        }
-        if (j > 0 && __any_sync(0xffffffffu, grow)) {
-          // the previous tile's P V must be in O before it is rescaled: the
-          // lane's tile-empty barrier of that tile completes with it
-          if (!wait_all(tc::kBarTEmpty + 4 * l + (g - 1) % C::kMStages,
-                        ((g - 1) / C::kMStages) & 1)) {
+        ev = e;
+        cur = mark;
+      };
+      // The tiles from j on.  4-bit: first without any of that, until a tile of
+      // another bin or a bad one (so the loop that nearly all tiles take has no
+      // more to do than over BF16 pages), then all others with it.
+      int j = 0;
+      auto tiles = [&](auto general) {
+        constexpr bool kAny = k16 && decltype(general)::value;
+        for (; j < ntl; ++j) {
+          const uint32_t g = G + j, gl = Gl + j;
+          const int s = static_cast<int>(g % C::kMStages);
+          int mark = 0;
+          if (k16) {   // (while the scores are on their way)
+            if (!wait_all(kBarTileFull + s, (g / C::kMStages) & 1)) {
+              dead = true;
+              return;
+            }
+            mark = tile_ok_of[s];
+            if (kAny) {
+              if (mark != 0 && mark != cur) rebin(mark);
+            } else if (mark != cur) {
+              return;
+            }
+          }
+          if (!wait_all(tc::kBarSFull + 2 * l + (gl & 1), (gl >> 1) & 1) ||
+              (!k16 && !wait_all(kBarTileFull + s, (g / C::kMStages) & 1))) {
             dead = true;
-            break;
+            return;
           }
           tc_fence_after();
+          uint32_t sr[64];
+          tmem_ld64(trow + 64 * (gl & 1), sr);
+          tmem_wait_ld();
+          const bool tile_ok = k16 ? !kAny || mark != 0 : tile_ok_of[s] != 0;
+          const int key0 = j * kPage;
+          // keys of this tile the row sees: 0 .. lim (none for lim < 0); only
+          // the tiles on a row's diagonal (or a bad tile) need the mask, which
+          // sets the other scores to -inf in place (a copy of the row would
+          // cost a move per score on the unmasked tiles)
+          const int lim = (valid && tile_ok) ? min(63, pos - key0) : -1;
+          if (!__all_sync(0xffffffffu, lim == 63)) {
 #pragma unroll
-          for (int qc = 0; qc < 4; ++qc) {
-            uint32_t ov[32];
-            tmem_ld32(trow + 128 + 32 * qc, ov);
-            tmem_wait_ld();
-#pragma unroll
-            for (int jk = 0; jk < 32; ++jk) ov[jk] = __float_as_uint(__uint_as_float(ov[jk]) * alpha);
-            tmem_st32(trow + 128 + 32 * qc, ov);
+            for (int jk = 0; jk < 64; ++jk)
+              if (jk > lim) sr[jk] = 0xff800000u;
           }
-        }
-        // p = 2^(s * scale - m) as one FMA and one exponential, packed as
-        // BF16 (F16 for E4M3 caches) pairs over the scores; the row sum in 4
-        // independent chains
-        {
-          const float nms = m_used == -INFINITY ? 0.f : -m_used;
-          const uint64_t scale2 = f32x2(scale_log2, scale_log2), nms2 = f32x2(nms, nms);
-          uint64_t ps2[4] = {0ull, 0ull, 0ull, 0ull};   // pairs of row sums
-          uint32_t pk[32];
+          // the row maximum of the raw scores, three-input maxima in 8
+          // independent chains (each started from a pair); the scale is
+          // positive, so it commutes with the maximum
+          float m8[8];
 #pragma unroll
-          for (int jk = 0; jk < 32; ++jk) {
-            float a0, a1;
-            f32x2_split(fma_f32x2(f32x2(__uint_as_float(sr[2 * jk]), __uint_as_float(sr[2 * jk + 1])),
-                                  scale2, nms2),
-                        a0, a1);
-            const float p0 = exp2_ftz(a0), p1 = exp2_ftz(a1);
-            ps2[jk & 3] = add_f32x2(ps2[jk & 3], f32x2(p0, p1));
-            pk[jk] = kFp8 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
+          for (int jk = 0; jk < 64; jk += 2) {
+            const int c = (jk >> 1) & 7;
+            const float a = __uint_as_float(sr[jk]), b = __uint_as_float(sr[jk + 1]);
+            m8[c] = jk < 16 ? fmaxf(a, b) : max3f(m8[c], a, b);
           }
-          tmem_st32(trow + 64 * (gl & 1), pk);
-          float s0, s1;
-          f32x2_split(add_f32x2(add_f32x2(ps2[0], ps2[1]), add_f32x2(ps2[2], ps2[3])), s0, s1);
-          lsum += s0 + s1;
+          const float mx =
+              max3f(max3f(m8[0], m8[1], m8[2]), max3f(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7])) *
+              scale_log2;
+          // the running maximum moves only when it grows by more than 2^8
+          // (weights stay <= 2^8); the row's O is then rescaled in TMEM
+          const bool grow = mx > m_used + tc::kRescaleLog2;
+          const float alpha = grow ? exp2_ftz(m_used - mx) : 1.f;   // 0 while m_used = -inf
+          if (grow) {
+            lsum *= kAny && shifted ? exp2_ftz(sum_ref - mx) : alpha;
+            m_used = mx;
+            if (kAny) sum_ref = mx;
+          }
+          if (j > 0 && __any_sync(0xffffffffu, grow)) {
+            // the previous tile's P V must be in O before it is rescaled: the
+            // lane's tile-empty barrier of that tile completes with it
+            if (!wait_all(tc::kBarTEmpty + 4 * l + (g - 1) % C::kMStages,
+                          ((g - 1) / C::kMStages) & 1)) {
+              dead = true;
+              return;
+            }
+            tc_fence_after();
+#pragma unroll
+            for (int qc = 0; qc < 4; ++qc) {
+              uint32_t ov[32];
+              tmem_ld32(trow + 128 + 32 * qc, ov);
+              tmem_wait_ld();
+#pragma unroll
+              for (int jk = 0; jk < 32; ++jk) ov[jk] = __float_as_uint(__uint_as_float(ov[jk]) * alpha);
+              tmem_st32(trow + 128 + 32 * qc, ov);
+            }
+          }
+          // p = 2^(s * scale - m) as one FMA and one exponential, packed as
+          // BF16 (F16 for E4M3 caches) pairs over the scores; the row sum in 4
+          // independent chains
+          {
+            float nms = m_used == -INFINITY ? 0.f : k16 ? tc::kLiftLog2 - m_used : -m_used;
+            float part = 1.f;   // of the row sum, for a sum of 1
+            bool far = false;
+            if (kAny && shifted) {
+              far = mx < m_used - tc::kFarLog2;
+              part = far                     ? exp2_ftz(mx + tc::kLiftLog2 - sum_ref)
+                     : m_used == -INFINITY ? 1.f
+                                           : exp2_ftz(m_used - sum_ref);
+              if (far) nms = mx == -INFINITY ? 0.f : -mx;
+            }
+            const uint64_t scale2 = f32x2(scale_log2, scale_log2), nms2 = f32x2(nms, nms);
+            uint64_t ps2[4] = {0ull, 0ull, 0ull, 0ull};   // pairs of row sums
+            uint32_t pk[32];
+#pragma unroll
+            for (int jk = 0; jk < 32; ++jk) {
+              float a0, a1;
+              f32x2_split(fma_f32x2(f32x2(__uint_as_float(sr[2 * jk]), __uint_as_float(sr[2 * jk + 1])),
+                                    scale2, nms2),
+                          a0, a1);
+              const float p0 = exp2_ftz(a0), p1 = exp2_ftz(a1);
+              ps2[jk & 3] = add_f32x2(ps2[jk & 3], f32x2(p0, p1));
+              pk[jk] = kFp8 || k16 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
+            }
+            if (kAny && __any_sync(0xffffffffu, far)) {
+#pragma unroll
+              for (int jk = 0; jk < 32; ++jk) pk[jk] = far ? 0u : pk[jk];
+            }
+            tmem_st32(trow + 64 * (gl & 1), pk);
+            float s0, s1;
+            f32x2_split(add_f32x2(add_f32x2(ps2[0], ps2[1]), add_f32x2(ps2[2], ps2[3])), s0, s1);
+            lsum += kAny ? (s0 + s1) * part : s0 + s1;
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(bar(tc::kBarPFull + 2 * l + (gl & 1)));
         }
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(bar(tc::kBarPFull + 2 * l + (gl & 1)));
+      };
+      if constexpr (k16) {
+        if (!take_q() || !wait_all(kBarTileFull + G % C::kMStages, (G / C::kMStages) & 1)) break;
+        const int mark = tile_ok_of[G % C::kMStages];
+        if (mark != 0) {
+          rebin(mark);
+          tiles(std::false_type{});
+        }
+        if (!dead && j < ntl) tiles(std::true_type{});
+      } else {
+        tiles(std::false_type{});
       }
       if (dead) break;
       // the row of O once the lane's last P V is done: divide by the row sum, store
       if (!wait_all(tc::kBarOFinal + l, Vl & 1)) break;
       tc_fence_after();
-      const float inv = lsum > 0.f ? v_scale / lsum : 0.f;
+      float inv = lsum > 0.f ? v_scale / lsum : 0.f;
+      if (k16) inv *= pow2(ev) * (shifted && m_used != -INFINITY ? exp2_ftz(m_used - sum_ref) : 1.f);
       const int64_t orow = (static_cast<int64_t>(qs + i) * kHq + head) * kD;
       if (out_dtype == HPC_OUT_FP32) {
 #pragma unroll
