@@ -90,9 +90,14 @@ typedef enum { HPC_OUT_BF16 = 0, HPC_OUT_FP16 = 1, HPC_OUT_FP32 = 2 } hpc_out_dt
  *   byte 8704 + ((t/2)*4 + d/32)*4 + (t%2)*2                  V scale (bf16)
  * Every call that takes a kv_dtype takes HPC_KV_INT4, except that its
  * attention query is bf16 (HPC_ERR_UNSUPPORTED for an E4M3 q; q must be
- * 16-byte aligned, sm_scale not negative), that the prologue wants q, k, v, the norm weights and q_out
- * 8-byte and cos_sin 16-byte aligned (HPC_ERR_INVALID_ARG otherwise), and that
- * hpc_prefill_attn needs its staged form. */
+ * 16-byte aligned, sm_scale not negative), that the prologue wants q, k, v, the
+ * norm weights and q_out 8-byte and cos_sin 16-byte aligned (HPC_ERR_INVALID_ARG
+ * otherwise), and that hpc_prefill_attn needs its staged form.  Sizes: the
+ * prologue sums a K row's squares in fp32, as for the other caches (elements
+ * below 2^60); the decode attention takes P times a V scale as bf16, so values
+ * of V keep their precision from 2^-100 to 2^100, and rows of q below 2^107 in
+ * magnitude (at sm_scale up to 1).  The slots of one prologue call must differ,
+ * negative ones apart: a slot written twice holds parts of both tokens. */
 
 /* Options of the _ex attention calls; NULL means the single-token BF16 form
  * ({1, HPC_Q_BF16, 1.0f, HPC_OUT_BF16}). */

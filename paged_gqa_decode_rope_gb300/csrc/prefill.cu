@@ -138,8 +138,8 @@ __global__ void __launch_bounds__(kStageThreads) stage_convert_kernel(
 // same staged pages.  A block takes one (page, KV head) record at a time: the 9 KB
 // land in shared memory coalesced, every warp takes the powers from the scales, then
 // every thread writes 16 bytes of a staged row a step (rows are read out of the
-// record's fragment order there, not from memory).  Bound by memory: the pages of 4 x 4096 tokens
-// 18 us, 86 MB in and out at 4.8 TB/s, before an attention of 722 us.
+// record's fragment order there, not from memory).  Bound by memory: the pages of
+// 4 x 4096 tokens 16 us, 86 MB in and out at 5.4 TB/s, before an attention of 777 us.
 __global__ void __launch_bounds__(kStageThreads) stage_convert_i4_kernel(
     const uint8_t* __restrict__ cache, int32_t num_blocks, const int32_t* __restrict__ block_table,
     int32_t max_blocks, const int32_t* __restrict__ seq_lens, int32_t batch,

@@ -7,17 +7,18 @@
 // store is 8 bytes a lane, a row's sum takes four shuffles for two rows at
 // once, and the table's sines and cosines are read once for a token's nine
 // rows of a warp.  K and V of the KV head are the two halves of one pass.
-// Bound by memory once there are enough tokens (33 KB of q in and out each),
-// with issue slots not far behind (750 instructions a warp): 8191 tokens take 66
-// us, 5.4 TB/s, at six blocks an SM (40 registers; four blocks 74, five 68); the
-// other caches' prologue, a warp per row with a quarter of the bytes in flight,
-// 98 us.
+// Memory (38.5 KB a token, 16 of q in and 16 out) and issue slots (750 instructions
+// a warp) come close to each other: 8191 tokens take 64 us, 5.0 TB/s, 0.74 of a
+// copy's rate, at six blocks an SM (40 registers; five blocks took 3 % more, four
+// 12 %); the other caches' prologue, a warp per row with a quarter of the bytes in
+// flight, 98 us.
 //
 // The codes are those of the exact k'.  In fp32 a value is known to
 // kI4RelErr: where scale or code could come out otherwise within that, about
 // one row in 300, the row is done again in pairs of floats (48 bits; that a
 // code still comes out wrong has odds of one in 10^10 a row), which takes a
-// fifth of the time of this part's 64-bit arithmetic.
+// fifth of the time of this part's 64-bit arithmetic.  So are groups with a scale
+// below 2^-100, times a power of two.
 #pragma once
 
 #include "int4.cuh"
