@@ -595,8 +595,9 @@ int hpc_prefill_attn(const void* q, int32_t num_tokens, const int32_t* query_sta
  * of two per page and head that the kernel takes back, and q and P are F16 in
  * the products: the only roundings are P's (2^-11) and the output's.  (Exact for
  * scales down to 2^-13 of the page's largest and above 2^-106, and for elements
- * of q down to 2^-25 of their row's largest.)  For a BF16 cache this is
- * hpc_prefill_attn (staging unused).
+ * of q down to 2^-25 of their row's largest.)  A NaN in a 4-bit cache reaches
+ * only the rows that see its token.  For a BF16 cache this is hpc_prefill_attn
+ * (staging unused).
  * Source: as hpc_prefill_attn.
  * Arguments as hpc_prefill_attn, and:
  *   staging        (device) [staging_pages][2][8][64][128] of 16 bits, 16-byte

@@ -79,24 +79,30 @@ __device__ __forceinline__ float i4_value(uint32_t w, int i, float s) {
 // `keep` tokens.  Code times scale is then below 57344, and an F16 value exactly
 // for scales down to 2^-13 of the largest at least, 2^-29 at most.  k is 0 for
 // scales of 2^-12 .. 2^4; not below kI4LowBin, where scales under 2^-106 are held
-// less exactly.  x: the words of the lane's tokens 2 lane and 2 lane + 1.
+// less exactly.  x: the words of the lane's tokens 2 lane and 2 lane + 1.  *nan: of
+// the first `keep` tokens, one has an infinity or a NaN.
 constexpr int kI4LowBin = -5;
 __device__ __forceinline__ int i4_bin_power(int bin) { return 9 - 16 * bin; }
 template <bool kV>
-__device__ __forceinline__ int i4_tile_bin(uint4 x, int lane, int keep) {
+__device__ __forceinline__ int i4_tile_bin(uint4 x, int lane, int keep, bool* nan) {
   const uint32_t w[4] = {x.x & 0x7fff7fffu, x.y & 0x7fff7fffu, x.z & 0x7fff7fffu, x.w & 0x7fff7fffu};
   uint32_t m = __vmaxu2(__vmaxu2(w[0], w[1]), __vmaxu2(w[2], w[3]));
   m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+  *nan = false;
   if (keep < kPage || m >= 0x7f80u) {
     // without the tokens past the end, and without infinities and NaN (K's second
     // token has words 2 and 3, V's the high halves)
     m = 0;
+    bool bad = false;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const uint32_t half = i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xffffu;
-      if (2 * lane + (kV ? i & 1 : i >> 2) < keep && half < 0x7f80u) m = max(m, half);
+      const bool live = 2 * lane + (kV ? i & 1 : i >> 2) < keep;
+      if (live && half < 0x7f80u) m = max(m, half);
+      bad = bad || (live && half >= 0x7f80u);
     }
     m = __reduce_max_sync(0xffffffffu, m);
+    *nan = __any_sync(0xffffffffu, bad);
   }
   return max((static_cast<int>(m >> 7) - 127 + 12) >> 4, kI4LowBin);
 }

@@ -139,8 +139,8 @@ __global__ void __launch_bounds__(kStageThreads) stage_convert_kernel(
 // land in shared memory coalesced, every warp takes the powers from the scales, then
 // every thread writes 16 bytes of a staged row a step (rows are read out of the
 // record's fragment order there, not from memory).  Bound by memory: the pages of
-// 4 x 4096 tokens 16 us, 86 MB in and out at 5.4 TB/s, before an attention of 777 us.
-__global__ void __launch_bounds__(kStageThreads) stage_convert_i4_kernel(
+// 4 x 4096 tokens 16 us, 86 MB in and out at 5.4 TB/s, before an attention of 781 us.
+__global__ void __launch_bounds__(kStageThreads, 6) stage_convert_i4_kernel(
     const uint8_t* __restrict__ cache, int32_t num_blocks, const int32_t* __restrict__ block_table,
     int32_t max_blocks, const int32_t* __restrict__ seq_lens, int32_t batch,
     const int32_t* __restrict__ page_ptr, int32_t staged_pages, uint16_t* __restrict__ staged) {
@@ -164,10 +164,11 @@ __global__ void __launch_bounds__(kStageThreads) stage_convert_i4_kernel(
     __syncthreads();
     const int lane = threadIdx.x & 31;
     const int keep = seq_lens[lo] - kPage * (pg - page_ptr[lo]);
+    bool nan;   // (V: see below)
     const float kp = pow2(i4_bin_power(
-        i4_tile_bin<false>(*reinterpret_cast<const uint4*>(rec + kI4OffKs + 16 * lane), lane, keep)));
+        i4_tile_bin<false>(*reinterpret_cast<const uint4*>(rec + kI4OffKs + 16 * lane), lane, keep, &nan)));
     const float vp = pow2(i4_bin_power(
-        i4_tile_bin<true>(*reinterpret_cast<const uint4*>(rec + kI4OffVs + 16 * lane), lane, keep)));
+        i4_tile_bin<true>(*reinterpret_cast<const uint4*>(rec + kI4OffVs + 16 * lane), lane, keep, &nan)));
     uint16_t* k_page = staged + (static_cast<int64_t>(pg) * 2 * kHkv + h) * kPage * kD;
     uint16_t* v_page = k_page + static_cast<int64_t>(kHkv) * kPage * kD;
 #pragma unroll
@@ -177,7 +178,10 @@ __global__ void __launch_bounds__(kStageThreads) stage_convert_i4_kernel(
       const float ks = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(rec + i4_ks_byte(t, g))) * kp;
       const uint32_t vw = *reinterpret_cast<const uint16_t*>(rec + i4_v_byte(t, d)) |
                           (static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(rec + i4_v_byte(t, d + 4))) << 16);
-      const float vs = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(rec + i4_vs_byte(t, g))) * vp;
+      // (zeros for a NaN in V: rows that do not see its token have P = 0 there, and
+      // 0 * NaN is NaN; the attention makes the rows that do NaN)
+      const float sv = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(rec + i4_vs_byte(t, g)));
+      const float vs = nan && !isfinite(sv) ? 0.f : sv * vp;
       uint32_t ko[4], vo[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {

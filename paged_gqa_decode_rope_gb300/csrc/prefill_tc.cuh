@@ -51,7 +51,8 @@
 // of 2^-24 below.  Where ev has changed within a unit, the row sum keeps a reference
 // of its own, and a tile whose products stay 2^-40 below the largest adds nothing to
 // O: its P is zero, and its part of the row sum is taken by its own maximum, as P
-// could underflow there.
+// could underflow there.  A NaN in V is staged as zeros, and the rows that see its
+// token get it in its group of 32 elements (others must not: 0 * NaN is NaN).
 #pragma once
 
 #include <type_traits>
@@ -147,6 +148,7 @@ constexpr float kRescaleLog2 = 8.0f;                // rescale O only when the m
 constexpr float kLiftLog2 = 7.0f;                   // 4-bit: P times 2^7, so at most 2^15
 constexpr float kFarLog2 = 40.0f;                   // 4-bit: a tile this far below adds nothing
 constexpr int kMarkBias = 16;                       // 4-bit: a good tile's mark holds the bins of K and V + 16
+constexpr int kMarkNan = 1 << 16;                   //        and whether a token's V has a NaN
 
 // tiles of a lane of a unit: 0 without new tokens, else those its last token sees
 __device__ __forceinline__ int lane_tiles(int qlen, int L, int first_token) {
@@ -385,8 +387,10 @@ __global__ void __launch_bounds__(tc::Cfg<kForm>::kThreads, 1) prefill_tc_kernel
           int mark = 1;
           if (k16) {
             const int keep = L - kPage * (tb + jj);
-            mark = (i4_tile_bin<false>(ks, lane, keep) + tc::kMarkBias) << 8 |
-                   (i4_tile_bin<true>(vs, lane, keep) + tc::kMarkBias);
+            bool nan;
+            const int k_bin = i4_tile_bin<false>(ks, lane, keep, &nan);
+            mark = (k_bin + tc::kMarkBias) << 8 | (i4_tile_bin<true>(vs, lane, keep, &nan) + tc::kMarkBias);
+            if (nan) mark |= tc::kMarkNan;   // (of V)
             if (jj + 1 < in_chunk) load_scales(jj + 1);
           }
           const int s = static_cast<int>(g % C::kPStages);
@@ -627,6 +631,7 @@ __global__ void __launch_bounds__(tc::Cfg<kForm>::kThreads, 1) prefill_tc_kernel
       int cur = 0, ev = 0;
       bool shifted = false;
       float sum_ref = 0.f;
+      unsigned nan = 0;   // bit g: the row sees a NaN in V's group g
       auto rebin = [&](int mark) {
         const int e = -i4_bin_power((mark & 0xff) - tc::kMarkBias);
         // (positive, as masked scores are -inf)
@@ -656,7 +661,8 @@ __global__ void __launch_bounds__(tc::Cfg<kForm>::kThreads, 1) prefill_tc_kernel
             }
             mark = tile_ok_of[s];
             if (kAny) {
-              if (mark != 0 && mark != cur) rebin(mark);
+              const int bins = mark & (tc::kMarkNan - 1);
+              if (bins != 0 && bins != cur) rebin(bins);
             } else if (mark != cur) {
               return;
             }
@@ -677,6 +683,20 @@ __global__ void __launch_bounds__(tc::Cfg<kForm>::kThreads, 1) prefill_tc_kernel
           // sets the other scores to -inf in place (a copy of the row would
           // cost a move per score on the unmasked tiles)
           const int lim = (valid && tile_ok) ? min(63, pos - key0) : -1;
+          if (kAny && (mark & tc::kMarkNan)) {
+            // (staged as zeros)
+            const int bid = block_table[static_cast<int64_t>(d.b) * max_blocks + j];
+            const uint4* vs = reinterpret_cast<const uint4*>(
+                kv_codes + (static_cast<int64_t>(bid) * kHkv + d.h) * kI4Record + kI4OffVs);
+#pragma unroll 1
+            for (int t = 0; t <= lim; t += 2) {   // a word a group, a half a token
+              const uint4 x = vs[t >> 1];
+              const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+              for (int gr = 0; gr < 4; ++gr)
+                if ((w[gr] & 0x7f80u) == 0x7f80u || (t < lim && (w[gr] >> 16 & 0x7f80u) == 0x7f80u)) nan |= 1u << gr;
+            }
+          }
           if (!__all_sync(0xffffffffu, lim == 63)) {
 #pragma unroll
             for (int jk = 0; jk < 64; ++jk)
@@ -768,7 +788,7 @@ __global__ void __launch_bounds__(tc::Cfg<kForm>::kThreads, 1) prefill_tc_kernel
         if (!take_q() || !wait_all(kBarTileFull + G % C::kMStages, (G / C::kMStages) & 1)) break;
         const int mark = tile_ok_of[G % C::kMStages];
         if (mark != 0) {
-          rebin(mark);
+          rebin(mark & (tc::kMarkNan - 1));
           tiles(std::false_type{});
         }
         if (!dead && j < ntl) tiles(std::true_type{});
@@ -781,6 +801,8 @@ __global__ void __launch_bounds__(tc::Cfg<kForm>::kThreads, 1) prefill_tc_kernel
       tc_fence_after();
       float inv = lsum > 0.f ? v_scale / lsum : 0.f;
       if (k16) inv *= pow2(ev) * (shifted && m_used != -INFINITY ? exp2_ftz(m_used - sum_ref) : 1.f);
+      // (of 32 columns, a group of V)
+      auto inv_of = [&](int qc) { return k16 && (nan >> qc & 1u) ? __uint_as_float(0x7fc00000u) : inv; };
       const int64_t orow = (static_cast<int64_t>(qs + i) * kHq + head) * kD;
       if (out_dtype == HPC_OUT_FP32) {
 #pragma unroll
@@ -793,7 +815,7 @@ __global__ void __launch_bounds__(tc::Cfg<kForm>::kThreads, 1) prefill_tc_kernel
             for (int jk = 0; jk < 32; jk += 8) {
               float v8[8];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) v8[e] = __uint_as_float(ov[jk + e]) * inv;
+              for (int e = 0; e < 8; ++e) v8[e] = __uint_as_float(ov[jk + e]) * inv_of(qc);
               store_out8(out, orow + 32 * qc + jk, v8, out_dtype);
             }
           }
@@ -819,8 +841,8 @@ __global__ void __launch_bounds__(tc::Cfg<kForm>::kThreads, 1) prefill_tc_kernel
             uint32_t w[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const float a = __uint_as_float(ov[8 * pc + 2 * k]) * inv;
-              const float b = __uint_as_float(ov[8 * pc + 2 * k + 1]) * inv;
+              const float a = __uint_as_float(ov[8 * pc + 2 * k]) * inv_of(qc);
+              const float b = __uint_as_float(ov[8 * pc + 2 * k + 1]) * inv_of(qc);
               w[k] = h16 ? pack_f16(a, b) : pack_bf16(a, b);
             }
             *reinterpret_cast<uint4*>(ebuf + lane * 64 + 16 * (pc ^ ((lane >> 1) & 3))) =

@@ -1,6 +1,7 @@
 """A NaN or an infinity in a query, or a NaN in a cached K, makes that row NaN,
 however the plan cuts its sequence, and leaves every other row as it is."""
 
+import numpy as np
 import pytest
 import torch
 
@@ -132,3 +133,59 @@ def test_prefill_query_that_is_not_finite(kv, staged):
             bad[i, 5] = bad[i, 62] = True
     assert bool(torch.isnan(outs[1][bad]).all()), outs[1][bad][:, 0].tolist()
     assert torch.equal(outs[1][~bad], outs[0][~bad])
+
+
+@pytest.mark.parametrize("out_dtype", [0, 2])
+def test_int4_prefill_nan_in_the_cache_reaches_who_sees_it(out_dtype):
+    """NaN in K of one new token, in groups of V of others: the tokens before them,
+    and other heads, do not see it."""
+    from paged_gqa_decode_rope_gb300 import ops
+    lens, new = [300, 200, 70], [300, 70, 70]
+    b = iu.Int4Batch(lens, 89)
+    iu.exact_keys(b)
+    clean = b.host.copy()
+
+    def spoil(which, s, t, h, groups):
+        for g in groups:
+            at = oi.scale_byte(which, t % 64, g)
+            b.host[b.table[s, t // 64], h, at:at + 2] = (0xC0, 0x7F)
+
+    spoil(1, 0, 41, 2, [1])           # V of token 41, group 1
+    spoil(1, 0, 230, 2, [0, 3])
+    spoil(0, 0, 100, 5, [2])          # K of token 100
+    spoil(1, 1, 150, 7, range(4))     # V of new token 20
+    b.to("cuda")
+    q = iu.queries((440, 64, 128), 90)
+    qst = torch.tensor([0, 300, 370, 440], dtype=torch.int32, device="cuda")
+    pf = ops.PrefillAttention(3, out_dtype=out_dtype, staging_pages=ops.PrefillAttention.pages_for(lens))
+    pf.plan(qst)
+    out = pf(q, qst, b.cache, INT4, None, b.block_table, b.seq_lens,
+             torch.empty(q.shape, dtype=ops._OUT_TORCH[out_dtype], device="cuda"))
+    assert int(pf.status.item()) == 0
+    gh, qh, dt = iu.host(out), iu.host(q), out.dtype
+
+    def row(s, i, h, nan):
+        """Token i of sequence s, a head of KV head h: groups of nan NaN, the others right."""
+        at, j = int(qst[s]) + i, 8 * h + i % 8
+        K, V = b.rows(s, h, clean)
+        want, size = iu.attention(qh[at, j], K, V, lens[s] - new[s] + i + 1)
+        bad = np.repeat(np.isin(np.arange(4), list(nan)), 32)
+        assert np.all(np.isnan(gh[at, j][bad])), (s, i, h)
+        if not bad.all():
+            iu.check(gh[at, j][~bad], want[~bad], size[~bad], dt, "seq %d token %d head %d" % (s, i, h))
+
+    for i, nan in ((0, []), (40, []), (41, [1]), (42, [1]), (63, [1]), (64, [1]), (229, [1]), (230, [0, 1, 3]),
+                   (299, [0, 1, 3])):
+        row(0, i, 2, nan)
+        row(0, i, 0, [])
+    for i in (0, 70, 99):
+        row(0, i, 5, [])
+    for i in (100, 101, 128, 299):
+        row(0, i, 5, range(4))
+    for i in (0, 19):
+        row(1, i, 7, [])
+    for i in (20, 69):
+        row(1, i, 7, range(4))
+        row(1, i, 6, [])
+    for i in (0, 69):
+        row(2, i, 3, [])
